@@ -19,11 +19,15 @@ weights registered in the packed tile layout ``proj_packed_bytes``,
 ``proj_num_candidates_packed``, ``proj_candidate_name_packed``,
 ``proj_run_candidate_packed``, the measured read floor
 ``proj_read_probe``, and ``proj_run_noalloc`` (proj_run with no device
-allocation).
+allocation); for 4-bit weights with group scales ``proj_pack_codes``,
+``proj_quantize_weights``, ``proj_run_quant``; and for the paged key-value
+cache between a decoding step's projections ``proj_kv_append`` and
+``proj_kv_attend`` on a cache described once by ``kv_cache``.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +43,7 @@ PROJ_ERR_DESTROYED = 6
 
 EPI_NONE, EPI_BIAS, EPI_GELU_TANH, EPI_BIAS_GELU_TANH = 0, 1, 2, 3
 OUT_F32, OUT_BF16 = 0, 1
+KV_BF16, KV_FP8 = 0, 1
 
 EXPORTS = ["proj_create", "proj_run", "proj_tune", "proj_destroy", "proj_status_string",
            "proj_last_error", "proj_get_plan", "proj_num_candidates", "proj_candidate_name",
@@ -46,7 +51,8 @@ EXPORTS = ["proj_create", "proj_run", "proj_tune", "proj_destroy", "proj_status_
            "proj_prepare_hilo", "proj_run_hilo", "proj_get_plan_hilo", "proj_num_candidates_hilo",
            "proj_candidate_name_hilo", "proj_run_candidate_hilo", "proj_packed_bytes", "proj_pack_weights",
            "proj_run_packed", "proj_get_plan_packed", "proj_num_candidates_packed", "proj_candidate_name_packed",
-           "proj_run_candidate_packed", "proj_read_probe", "proj_run_noalloc"]
+           "proj_run_candidate_packed", "proj_read_probe", "proj_run_noalloc",
+           "proj_pack_codes", "proj_quantize_weights", "proj_run_quant", "proj_kv_append", "proj_kv_attend"]
 
 
 class ProjError(RuntimeError):
@@ -54,6 +60,14 @@ class ProjError(RuntimeError):
         super().__init__("%s (status %d)%s" % (_status_text(status), status,
                                                ": " + message if message else ""))
         self.status = status
+
+
+class _KvCache(ctypes.Structure):
+    """proj_kv_cache of include/proj.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("pages", ctypes.c_int64),
+                ("k_strides", ctypes.c_int64 * 3), ("v_strides", ctypes.c_int64 * 3), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -100,6 +114,11 @@ def lib() -> ctypes.CDLL:
         "proj_run_candidate_packed": ([vp, ci, vp, vp, ci, vp, ci, i64, i64, i64, vp, ci, vp], st),
         "proj_read_probe": ([vp, vp, ctypes.c_size_t, vp], st),
         "proj_run_noalloc": (run_args, st),
+        "proj_pack_codes": ([vp, vp, i64, i64, vp, vp], st),
+        "proj_quantize_weights": ([vp, vp, i64, i64, ci, vp, vp, ci, vp, vp], st),
+        "proj_run_quant": ([vp, vp, vp, vp, ci, vp, ci, vp, ci, i64, i64, i64, vp, ci, vp], st),
+        "proj_kv_append": ([vp, vp, vp, i64, i64, ci, vp, i64, ci, ci, vp, vp, vp, vp], st),
+        "proj_kv_attend": ([vp, vp, vp, i64, i64, ci, vp, i64, i64, vp, i64, i64, ctypes.c_float, vp, ci, vp, vp], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -378,6 +397,176 @@ def proj_run_candidate_packed(ctx, index, X, Wp, tile16, bias, epilogue, Y, N, M
     _check(lib().proj_run_candidate_packed(ctx, int(index), _ptr(X), _ptr(Wp), int(tile16), _ptr(bias),
                                            int(epilogue), M, int(N), K, _ptr(Y), _out_dtype(Y, out_dtype),
                                            _stream(stream)), ctx)
+
+
+# ------------------------------------------- 4-bit weights, group scales
+
+def _is_tensor(name, t, dtypes, shape=None):
+    """Raise ValueError unless t is a device tensor of one of `dtypes` and, where given, of `shape`."""
+    if not t.is_cuda:
+        raise ValueError("%s must be on a GPU" % name)
+    if t.dtype not in dtypes:
+        raise ValueError("%s must be %s, got %s" % (name, " or ".join(map(str, dtypes)), t.dtype))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def proj_pack_codes(ctx, q, codes=None, stream=None):
+    """Lay out 4-bit codes given one to a byte (uint8 [N, K], K a multiple of
+    8) as int32 words [N, K / 8] (allocated here if not given): of eight
+    codes, code j sits at bits 4 * (j // 2) + 16 * (j % 2).  Returns them."""
+    import torch
+    _is_tensor("q", q, (torch.uint8,))
+    if q.dim() != 2 or q.shape[1] % 8:
+        raise ValueError("q must be uint8 [N, K] with K a multiple of 8")
+    N, K = q.shape
+    if codes is None:
+        codes = torch.empty((N, K // 8), dtype=torch.int32, device=q.device)
+    _is_tensor("codes", codes, (torch.int32,), (N, K // 8))
+    _check(lib().proj_pack_codes(ctx, _ptr(q), N, K, _ptr(codes), _stream(stream)), ctx)
+    return codes
+
+
+def proj_quantize_weights(ctx, W, group=128, zeros=True, scale_dtype=None, stream=None):
+    """4-bit weights of bf16 W [N, K]: (codes int32 [N, K / 8], scales
+    [N, G], zeros uint8 [N, G] or None), G = ceil(K / group).  With zeros=False every zero
+    point is 8; scales are bf16 unless scale_dtype is torch.float32."""
+    import torch
+    _is_tensor("W", W, (torch.bfloat16,))
+    if W.dim() != 2 or W.shape[1] % 8 or group not in (32, 64, 128):
+        raise ValueError("W must be bfloat16 [N, K] with K a multiple of 8, group 32, 64 or 128")
+    dt = torch.bfloat16 if scale_dtype is None else scale_dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError("scale_dtype must be bfloat16 or float32")
+    N, K = W.shape
+    G = -(-K // group)
+    codes = torch.empty((N, K // 8), dtype=torch.int32, device=W.device)
+    scales = torch.empty((N, G), dtype=dt, device=W.device)
+    z = torch.empty((N, G), dtype=torch.uint8, device=W.device) if zeros else None
+    _check(lib().proj_quantize_weights(ctx, _ptr(W), N, K, int(group), _ptr(codes), _ptr(scales),
+                                       OUT_F32 if dt == torch.float32 else OUT_BF16, _ptr(z), _stream(stream)), ctx)
+    return codes, scales, z
+
+
+def proj_run_quant(ctx, X, codes, scales, zeros, group, bias, epilogue, Y, stream=None) -> None:
+    """Enqueue Y = epilogue(X . W^T [+ bias]) with 4-bit W[n, k] =
+    scales[n, k // group] * (code[n, k] - zeros[n, k // group]) (zeros None:
+    8).  X bf16 [M, K], codes int32 [N, K / 8], scales bf16 or float32 and
+    zeros uint8 [N, ceil(K / group)], bias bf16 [N] or None, Y float32 /
+    bfloat16 [M, N]; all contiguous device tensors."""
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    _is_tensor("X", X, (bf16,))
+    _is_tensor("codes", codes, (torch.int32,))
+    if X.dim() != 2 or codes.dim() != 2 or group not in (32, 64, 128):
+        raise ValueError("X [M, K] and codes [N, K / 8] must have two dimensions, group 32, 64 or 128")
+    M, K = X.shape
+    N, words = codes.shape
+    if words * 8 != K:
+        raise ValueError("codes of %d words to a row do not fit K = %d" % (words, K))
+    G = -(-K // group)
+    _is_tensor("scales", scales, (bf16, f32), (N, G))
+    if zeros is not None:
+        _is_tensor("zeros", zeros, (torch.uint8,), (N, G))
+    if bias is not None:
+        _is_tensor("bias", bias, (bf16,), (N,))
+    _is_tensor("Y", Y, (bf16, f32), (M, N))
+    _check(lib().proj_run_quant(ctx, _ptr(X), _ptr(codes), _ptr(scales), OUT_F32 if scales.dtype == f32 else OUT_BF16,
+                                _ptr(zeros), group, _ptr(bias), epilogue, M, N, K, _ptr(Y),
+                                OUT_F32 if Y.dtype == f32 else OUT_BF16, _stream(stream)), ctx)
+
+
+# ------------------------------------------------- paged key-value cache
+
+class kv_cache:
+    """A paged cache in the caller's tensors k and v [pages, heads, page_size,
+    head_dim], bfloat16 or float8_e4m3fn (values = stored * scale).  Any
+    strides with a contiguous head: pages stored token-major are passed as
+    `k.transpose(1, 2)`.  Built once and used by every call; it keeps k and v
+    alive."""
+
+    def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
+        import torch
+        for name, t in (("k", k), ("v", v)):
+            _is_tensor(name, t, (torch.bfloat16, torch.float8_e4m3fn))
+            if t.dim() != 4 or (t.numel() and t.stride(3) != 1):
+                raise ValueError("%s must be [pages, heads, page_size, head_dim] with contiguous heads" % name)
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v differ in shape, dtype or device")
+        self.k, self.v = k, v
+        self.pages, self.heads, self.page_size, self.head_dim = k.shape
+        s3 = ctypes.c_int64 * 3
+        self._c = _KvCache(k.data_ptr(), v.data_ptr(), KV_FP8 if k.dtype == torch.float8_e4m3fn else KV_BF16, self.heads,
+                           self.head_dim, self.page_size, self.pages, s3(*k.stride()[:3]), s3(*v.stride()[:3]),
+                           float(k_scale), float(v_scale))
+        self._p = ctypes.addressof(self._c)
+
+
+def _rows(name, t):
+    """Pointer and row stride (elements) of a tensor whose rows are contiguous."""
+    if t.is_contiguous():
+        return t.data_ptr(), t[0].numel() if t.shape[0] else math.prod(t.shape[1:])
+    if not t[0].is_contiguous():
+        raise ValueError("%s must have contiguous rows" % name)
+    return t.data_ptr(), t[0].numel() if t.shape[0] == 1 else t.stride(0)
+
+
+def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=None, interleaved=False,
+                   stream=None) -> None:
+    """Enqueue one append: of qkv bf16 [T, (q_heads + 2 * heads) * head_dim]
+    (rows may be strided) the query and key heads are rotated by the rows
+    `positions` (int32 [T]) of rope float32 [positions, rot] (cosines, then
+    sines); queries go to q_out bf16 [T, q_heads, head_dim] (None: dropped),
+    keys and values into the cache's slots (int64 [T], page * page_size +
+    place; negative: a padding token, not stored)."""
+    import torch
+    _is_tensor("qkv", qkv, (torch.bfloat16,))
+    if qkv.dim() != 2:
+        raise ValueError("qkv must be [T, width]")
+    T, width = qkv.shape
+    heads = width // cache.head_dim - 2 * cache.heads
+    if width % cache.head_dim or heads < 0 or (q_heads is not None and q_heads != heads):
+        raise ValueError("qkv of width %d does not hold %s query and 2 * %d key-value heads of %d" %
+                         (width, "any" if q_heads is None else q_heads, cache.heads, cache.head_dim))
+    _is_tensor("rope", rope, (torch.float32,))
+    if rope.dim() != 2:
+        raise ValueError("rope must be [positions, rot]")
+    _is_tensor("positions", positions, (torch.int32,), (T,))
+    _is_tensor("slots", slots, (torch.int64,), (T,))
+    if q_out is not None:
+        _is_tensor("q_out", q_out, (torch.bfloat16,), (T, heads, cache.head_dim))
+    x, stride = _rows("qkv", qkv)
+    _check(lib().proj_kv_append(ctx, cache._p, x, stride, T, heads, _ptr(rope), rope.shape[0], rope.shape[1],
+                                1 if interleaved else 0, _ptr(positions), _ptr(slots), _ptr(q_out), _stream(stream)), ctx)
+
+
+def proj_kv_attend(ctx, cache, q, tables, lengths, scale, out, lse=None, window=0, max_len=None, stream=None) -> None:
+    """Enqueue attention of one new token for each of B sequences: q bf16
+    [B, q_heads, head_dim] (rows may be strided), tables int32 [B, width] the
+    sequences' pages, lengths int32 [B] their tokens (0: a padding place, out
+    0), the last `window` of them seen (0: all); out float32 / bfloat16
+    [B, q_heads, head_dim], lse float32 [B, q_heads] or None.  max_len bounds
+    the lengths (default: what the tables hold); a tight one gives a better
+    split."""
+    import torch
+    f32 = torch.float32
+    _is_tensor("q", q, (torch.bfloat16,))
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [B, q_heads, %d]" % cache.head_dim)
+    B, heads, _ = q.shape
+    _is_tensor("tables", tables, (torch.int32,))
+    if tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError("tables must be [B, width]")
+    _is_tensor("lengths", lengths, (torch.int32,), (B,))
+    _is_tensor("out", out, (torch.bfloat16, f32), q.shape)
+    if lse is not None:
+        _is_tensor("lse", lse, (f32,), (B, heads))
+    qp, stride = _rows("q", q)
+    tp, tstride = _rows("tables", tables)
+    tw = tables.shape[1]
+    _check(lib().proj_kv_attend(ctx, cache._p, qp, stride, B, heads, tp, tstride, tw, _ptr(lengths),
+                                tw * cache.page_size if max_len is None else max_len, window, scale, _ptr(out),
+                                OUT_F32 if out.dtype == f32 else OUT_BF16, _ptr(lse), _stream(stream)), ctx)
 
 
 def proj_graph_capture(ctx, Xs, Ws, biases, Ys, epilogue, out_dtype=None, stream=None) -> int:

@@ -27,6 +27,7 @@
 #include <vector>
 
 #include "../../include/proj.h"
+#include "context.hpp"
 #include "kernels.hpp"
 
 using namespace proj;
@@ -183,21 +184,6 @@ proj_status hip_fail(proj_ctx *c, const char *what, hipError_t e) {
     set_err(c, "%s: %s", what, hipGetErrorString(e));
     return PROJ_ERR_HIP;
 }
-
-class DeviceGuard {
-   public:
-    explicit DeviceGuard(int dev) {
-        if (hipGetDevice(&prev_) != hipSuccess) prev_ = -1;
-        if (prev_ != dev) hipSetDevice(dev);
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev_ >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev_) hipSetDevice(prev_);
-    }
-
-   private:
-    int prev_ = -1;
-};
 
 // largest M offered to the streaming kernel (in 64- or 128-row blocks)
 constexpr int64_t kStreamMaxM = 512;
@@ -433,13 +419,6 @@ hipError_t launch(const Candidate &cand, const Args &a, hipStream_t st) {
         case KIND_GEMV: return kGemvVariants[cand.variant].launch(a, cand.splits, st);
         default: return launch_generic(a, st);
     }
-}
-
-// Whether byte ranges [a, a + na) and [b, b + nb) share a byte.
-bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return pa < pb + nb && pb < pa + na;
 }
 
 // K is the product depth (twice the X row length for a hi/lo pair); wpack
@@ -840,6 +819,28 @@ hipError_t scratch_address(int device, void **out) {
 }
 
 }  // namespace
+
+namespace proj {
+
+proj_status context_view(proj_ctx *c, ContextView *v) {
+    if (!c) return PROJ_ERR_INVALID_ARG;
+    if (c->magic == kDead) return PROJ_ERR_DESTROYED;
+    if (c->magic != kMagic) return PROJ_ERR_INVALID_ARG;
+    *v = ContextView{c->device, c->cus, c->ws, c->ws_bytes};
+    return PROJ_OK;
+}
+
+proj_status context_error(proj_ctx *c, proj_status s, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    c->err = buf;
+    return s;
+}
+
+}  // namespace proj
 
 extern "C" {
 

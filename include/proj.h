@@ -259,6 +259,108 @@ proj_status proj_run_candidate_packed(proj_ctx *ctx, int index, const void *X, c
                                       const void *bias, int epilogue, int64_t M, int64_t N, int64_t K,
                                       void *Y, int out_dtype, void *stream);
 
+/* ---- 4-bit weights with group scales (what a decoding step reads most is
+ * weights: 4-bit codes take about 0.28 of the bytes of bf16 ones).
+ *
+ * W[n, k] = s[n, k / group] * (c[n, k] - z[n, k / group]), with c in 0..15,
+ * group 32, 64 or 128, and G = ceil(K / group) groups to a row (the last one
+ * may be short).  K is a multiple of 8.
+ *   codes   uint32 [N][K / 8]: of eight codes k = 8 i .. 8 i + 7, code j sits
+ *           at bits 4 * (j / 2) + 16 * (j % 2) of word i (so that the word
+ *           shifted by 4 p holds the pair 2 p, 2 p + 1 in its two halves)
+ *   scales  bf16 or fp32 [N][G] (a proj_out_dtype names the type)
+ *   zeros   uint8 [N][G], 0..15, or NULL: every z is 8
+ *
+ * proj_pack_codes lays out codes given one to a byte: q uint8 [N][K] (low
+ * four bits used) -> codes.  proj_quantize_weights makes all three from bf16
+ * W [N][K]: with zeros, lo = min(0, min W), hi = max(0, max W) of the group,
+ * s = (hi - lo) / 15 rounded to the scales' type, z = rint(-lo / s),
+ * c = rint(W / s) + z; without (zeros NULL), s = max|W| / 7 and z = 8; both
+ * clamped to 0..15, a group of zeros having s = 0 and c = z.  Every
+ * operand stays owned by the caller; N = 0 or K = 0 is a no-op. */
+proj_status proj_pack_codes(proj_ctx *ctx, const uint8_t *q, int64_t N, int64_t K, uint32_t *codes, void *stream);
+proj_status proj_quantize_weights(proj_ctx *ctx, const void *W, int64_t N, int64_t K, int group, uint32_t *codes,
+                                  void *scales, int scale_dtype, uint8_t *zeros, void *stream);
+
+/* Y = epilogue(X . W^T (+ bias)) for X bf16 [M][K] and 4-bit W as above.
+ * Epilogue, output types, M = 0, N = 0, K = 0 and overlap rules as proj_run.
+ * Products of X with the codes are exact, sums are fp32, the scales are
+ * applied to the fp32 sums of a group: nothing is rounded to bf16 before the
+ * output.  Allocates nothing and never synchronises, so it may be captured;
+ * which kernel runs follows from sizes and alignment alone (no tuning, no
+ * plan), so the same call gives the same bits every time.  Codes that are not
+ * 4-byte aligned, scales or X not aligned to their type: PROJ_ERR_INVALID_ARG. */
+proj_status proj_run_quant(proj_ctx *ctx, const void *X, const uint32_t *codes, const void *scales, int scale_dtype,
+                           const uint8_t *zeros, int group, const void *bias, int epilogue, int64_t M, int64_t N,
+                           int64_t K, void *Y, int out_dtype, void *stream);
+
+/* ---- Paged key-value cache: what runs between a decoding step's QKV
+ * projection and its output projection.
+ *
+ * A cache is the caller's memory: `pages` pages of `page_size` tokens (a power
+ * of two) for `heads` key-value heads of `head_dim` (64, 80, 96, 128, 192 or
+ * 256) elements.  Element d of head h, token t of page p sits at element
+ * p * strides[0] + h * strides[1] + t * strides[2] + d of k (v), so pages may
+ * be head-major or token-major; strides are multiples of 8 (bf16) or 16
+ * (fp8) elements and k and v 16-byte aligned.  PROJ_KV_FP8 holds OCP e4m3 values: the value is the
+ * stored one times k_scale (v_scale); for PROJ_KV_BF16 the scales are 1. */
+typedef enum {
+    PROJ_KV_BF16 = 0,
+    PROJ_KV_FP8 = 1 /* e4m3, values = stored * scale */
+} proj_kv_dtype;
+
+typedef struct {
+    void *k, *v;
+    int32_t dtype; /* a proj_kv_dtype */
+    int32_t heads, head_dim, page_size;
+    int64_t pages;
+    int64_t k_strides[3], v_strides[3]; /* page, head, token; in elements */
+    float k_scale, v_scale;
+} proj_kv_cache;
+
+/* Rotary positions applied to a fused projection's rows, and its keys and
+ * values stored: qkv bf16, row t at qkv + t * qkv_stride elements, holds
+ * q_heads query heads, then cache->heads key heads, then cache->heads value
+ * heads, each head_dim long.  Of each query and key head the first `rot`
+ * elements (even, 0..head_dim) are rotated in pairs: with interleaved = 0 the
+ * pair j < rot / 2 is (j, j + rot / 2), else (2 j, 2 j + 1); with cos and sin
+ * from row positions[t] of `rope` (fp32 [rope_rows][rot]: rot / 2 cosines,
+ * then rot / 2 sines), (a, b) -> (a cos - b sin, b cos + a sin) in fp32.
+ * Queries go to q_out bf16 [T][q_heads][head_dim] (NULL: not written; it may
+ * not overlap qkv or the cache).  Keys and values go to slot slots[t] = page *
+ * page_size + place: rounded to nearest even; for fp8 divided by the scale and
+ * clamped to +-448 first (NaN stays).  A negative slot marks a padding token,
+ * which is not stored.  A slot past the cache is not stored either.  A
+ * position outside the table makes that token's q_out row NaN and stores
+ * nothing.  Two tokens with one slot: either may remain.  Allocates nothing
+ * and never synchronises. */
+proj_status proj_kv_append(proj_ctx *ctx, const proj_kv_cache *cache, const void *qkv, int64_t qkv_stride, int64_t T,
+                           int q_heads, const float *rope, int64_t rope_rows, int rot, int interleaved,
+                           const int32_t *positions, const int64_t *slots, void *q_out, void *stream);
+
+/* Attention of one new token for each of B sequences over its pages: query
+ * head h reads key-value head h / (q_heads / cache->heads);
+ *     w[t] = scale * <q, k[t]>,  out = sum_t softmax(w)[t] v[t],
+ *     lse = log sum_t exp(w[t]),
+ * over t in [max(0, n - window), n) (window 0: all) with n = lengths[b].
+ * Token t is in page tables[b * table_stride + t / page_size].  n = 0 (a
+ * padding place): out = 0, lse = -infinity.  What lies outside that range, in
+ * the table or the cache, is not used, NaN included.  n above max_len, n < 0,
+ * or a page of the range outside the cache: that sequence's out and lse are
+ * NaN and nothing outside the cache is read.  max_len (at most table_width *
+ * page_size) bounds the lengths and shapes the launch.  q bf16: row b at
+ * q + b * q_stride, heads contiguous; out fp32 or bf16 [B][q_heads][head_dim];
+ * lse fp32 [B][q_heads] or NULL.  Sums and softmax are fp32, and the
+ * probabilities meet the values at full fp32 accuracy.  The split over the
+ * length follows from B, heads, max_len, window and the context's workspace,
+ * which holds the parts' fp32 results (with none, nothing is split): the same
+ * call gives the same bits every time.  Allocates nothing and never
+ * synchronises. */
+proj_status proj_kv_attend(proj_ctx *ctx, const proj_kv_cache *cache, const void *q, int64_t q_stride, int64_t B,
+                           int q_heads, const int32_t *tables, int64_t table_stride, int64_t table_width,
+                           const int32_t *lengths, int64_t max_len, int64_t window, float scale, void *out,
+                           int out_dtype, float *lse, void *stream);
+
 /* Free the context's device memory and plans (synchronises its device
  * first).  The handle itself stays allocated (a few hundred bytes) as a
  * marker: any later call with it, a second destroy included, returns
