@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libproj.so")
 SOURCES = ["proj.cpp", "stream.hip", "gemm.hip", "gemv.hip", "generic.hip",
-           "decode.cpp", "quant.hip", "kvcache.hip"]
+           "decode.cpp", "quant.hip", "kvcache.hip", "attend.hip"]
 
 
 def hipcc() -> str:

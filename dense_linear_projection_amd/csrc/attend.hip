@@ -1,0 +1,473 @@
+// attend.hip -- attention of one new token for each sequence over its pages
+// of a key-value cache, split over the length and joined.
+//
+// For a key-value head and the `per` query heads that share it, over the
+// tokens t of one part of the length,
+//     w[t][h] = scale <q[h], k[t]>,  m = max_t w,  l = sum_t exp(w - m),
+//     o[h][:] = sum_t exp(w[t][h] - m) v[t][:],
+// and parts with (m, l, o) join as (M = max m, sum 2^(m - M) l, ...): one
+// pass over keys and values, which bound the call (each is read once for
+// `per` query heads: about per operations a byte, far below the matrix
+// cores' rate).  Exponents are kept in base 2.
+//
+// A workgroup is four waves on one (sequence, key-value head, part); wave w
+// takes tiles w, w + 4, ... of 32 tokens, with its own running maximum, sum
+// and output, joined through LDS at the end, so the loop has no barrier.
+//   * w: v_mfma_f32_16x16x32_bf16 with A = 16 tokens of K, straight from
+//     global memory into registers (lane l: token l % 16, 8 elements), and
+//     B = 16 heads of q, held for the whole call.  A lane of the result has
+//     head l % 16 and tokens 4 (l / 16) + r.
+//   * o: A = V transposed (16 elements of the head x 32 tokens), B = the
+//     probabilities.  Two results of the first product, as they lie, are the
+//     32 tokens of B if slot 8 g + i of the product's k axis is token
+//     4 g + i (i < 4) or 16 + 4 g + i - 4; V follows by being read in that
+//     order with LDS's transposing loads.  So the probabilities never leave
+//     the registers.
+//   * a probability enters as two bf16 terms, its upper 8 bits (cut, so that
+//     the rest is never negative) and the rest rounded: 2^-16 of its value at
+//     most is lost, below what the fp32 sum of a logit loses.  The
+//     second term is at least 1e-37 so that an infinite value does not meet
+//     a zero.
+//   * K and V of the next tile are loaded while this one is computed: 16 KB
+//     a wave in flight at 128 elements in bf16, and nothing waits for anything
+//     but its own operands.
+// The running maximum moves only when a logit passes it by 2^8: sums stay in
+// range, and most tiles need no rescaling and no exchange between lanes.
+#include "decode.hpp"
+
+namespace proj {
+
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
+typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
+typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
+typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+
+constexpr int kChunk = 1024;       // tokens whose pages are staged at once
+constexpr float kLowest = -3e38f;  // a running maximum before the first logit
+
+// Four e4m3 bytes -> bf16, exact; two 32-bit words of pairs.
+__device__ __forceinline__ u32x2 fp8x4_to_bf16(uint32_t w) {
+    u32x2 r;
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+    return r;
+}
+
+__device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi) {
+    const u32x2 a = fp8x4_to_bf16(lo), b = fp8x4_to_bf16(hi);
+    return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int D, bool FP8, int QT>
+struct AttendCfg {
+    static constexpr int ROW = D * (FP8 ? 1 : 2);        // bytes of a token
+    static constexpr int NC = ROW / 16;                  // its 16-byte chunks
+    static constexpr int KS = (D + 31) / 32;             // steps of the first product
+    static constexpr int DT = D / 16;                    // tiles of the second
+    static constexpr int VI = (32 * NC + 63) / 64;       // chunks of V to a lane
+    static constexpr int TILE = 32 * ROW;                // bytes of a tile of V in LDS
+    static constexpr int ORED = 4 * 16 * (D + 4) * 4;    // the waves' outputs, 16 heads at a time
+    static constexpr int LDS = 4 * TILE > ORED ? 4 * TILE : ORED;
+    // rows after which a row starts at the same LDS bank again
+    static constexpr int PERIOD = ROW % 256 == 0 ? 1 : ROW % 128 == 0 ? 2 : ROW % 64 == 0 ? 4 : ROW % 32 == 0 ? 8 : 16;
+    // where chunk c of row r lies: turned by the row, so that the rows of one transposing load fall on different banks
+    static __device__ __forceinline__ int place(int c, int r) {
+        const int turn = FP8 ? r / PERIOD + (r >= 16 ? 4 : 0) : 2 * (r / PERIOD);
+        return (c + turn) % NC;
+    }
+    // first element of the 8 that lane group g has in step i (the same order for q and k)
+    static __device__ __forceinline__ int element(int i, int g) {
+        return FP8 && i < 2 * (D / 64) ? 64 * (i / 2) + 16 * g + 8 * (i % 2) : 32 * i + 8 * g;
+    }
+};
+
+// First token of a sequence that is seen, and how many parts its tokens make.
+__device__ __forceinline__ int64_t first_seen(const AttendArgs &a, int64_t n) {
+    return a.window > 0 && n > a.window ? n - a.window : 0;
+}
+__device__ __forceinline__ int parts_of(const AttendArgs &a, int64_t n) {
+    if (n <= 0 || n > a.max_len) return 0;
+    return static_cast<int>((n - first_seen(a, n) + a.part - 1) / a.part);
+}
+
+// Four elements of a finished head (and, with the first, its logarithm of the sum).
+__device__ __forceinline__ void finish_head(const AttendArgs &a, int64_t at, int64_t row, int d, f32x4 v, float most,
+                                            float total) {
+    const float f = total == 0.f ? 0.f : a.c.v_scale / total;
+    v = total == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * f;
+    if (a.out_dtype == OUT_F32) {
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = v;
+    } else {
+        const uint32_t lo = f32_to_bf16_bits(v[0]) | static_cast<uint32_t>(f32_to_bf16_bits(v[1])) << 16;
+        const uint32_t hi = f32_to_bf16_bits(v[2]) | static_cast<uint32_t>(f32_to_bf16_bits(v[3])) << 16;
+        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at) = u32x2{lo, hi};
+    }
+    if (d == 0 && a.lse)
+        a.lse[row] = total == 0.f ? -__builtin_inff() : (most + log2f(total)) * 0.6931471805599453f;
+}
+
+template <int D, bool FP8, int QT>
+__global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
+    using C = AttendCfg<D, FP8, QT>;
+    __shared__ __attribute__((aligned(16))) char lds[C::LDS];
+    __shared__ uint32_t pages[kChunk + 2];
+    __shared__ float top[4][16], sum[4][16];
+    __shared__ int wrong;
+
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int per = a.q_heads / a.c.heads;
+    // workgroup -> (sequence, part, head, chunk of the head's queries), heads fastest
+    const uint32_t hh = static_cast<uint32_t>(a.c.heads * a.chunks), u = blockIdx.x / hh, hc = blockIdx.x % hh;
+    const int64_t b = u / static_cast<uint32_t>(a.parts);
+    const int part = static_cast<int>(u % static_cast<uint32_t>(a.parts));
+    const int h = static_cast<int>(hc) / a.chunks, q0 = static_cast<int>(hc) % a.chunks * (16 * QT);
+    const int64_t n = a.lengths[b];
+    const int parts = parts_of(a, n);
+    if (part >= (parts > 0 ? parts : 1)) return;
+    const int64_t first = first_seen(a, n) + part * a.part;
+    const int64_t last = parts == 0 ? first : n < first + a.part ? n : first + a.part;
+    if (tid == 0) wrong = n < 0 || n > a.max_len;
+
+    bf16x8 q[QT][C::KS];
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int i = 0; i < C::KS; ++i) {
+            const int hq = q0 + 16 * t + c16, e = C::element(i, g);
+            q[t][i] = bf16x8{};
+            if (hq < per && e < D) q[t][i] = load16(a.q + b * a.q_stride + (static_cast<int64_t>(h) * per + hq) * D + e);
+        }
+    f32x4 o[QT][C::DT];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        m[t] = kLowest;
+        l[t] = 0.f;
+#pragma unroll
+        for (int i = 0; i < C::DT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const char *kb = static_cast<const char *>(a.c.k) + h * a.c.kh * (FP8 ? 1 : 2);
+    const char *vb = static_cast<const char *>(a.c.v) + h * a.c.vh * (FP8 ? 1 : 2);
+    const int64_t place_mask = (int64_t{1} << a.c.page_shift) - 1;
+    const float to_exp2 = a.scale * a.c.k_scale * 1.4426950408889634f;
+    char *vt = lds + wave * C::TILE;
+    u32x4 kr[2][FP8 ? (C::KS + 1) / 2 : C::KS], vr[C::VI];
+
+    for (int64_t base = first; base < last; base += kChunk) {
+        const int64_t end = last < base + kChunk ? last : base + kChunk;
+        const int64_t page0 = base >> a.c.page_shift;
+        const int npages = static_cast<int>(((end - 1) >> a.c.page_shift) - page0) + 1;
+        __syncthreads();  // the pages of the chunk before are no longer read
+        for (int i = tid; i < npages; i += 256) {
+            const int32_t p = a.tables[b * a.table_stride + page0 + i];
+            const bool ok = p >= 0 && p < a.c.pages;
+            pages[i] = ok ? static_cast<uint32_t>(p) : 0u;
+            if (!ok) wrong = 1;
+        }
+        __syncthreads();
+        if (wrong) break;  // nothing is read through a wrong table
+        const int tiles = static_cast<int>((end - base + 31) / 32), left = static_cast<int>(end - base);
+        const int in_page = static_cast<int>(base & place_mask);
+
+        // byte offset of a token of the chunk (one past its end: the last one, masked later)
+        auto offset = [&](int t, int64_t page_stride, int64_t token_stride) -> int64_t {
+            const int at = in_page + (t < left ? t : left - 1);
+            const int64_t e = static_cast<int64_t>(pages[at >> a.c.page_shift]) * page_stride +
+                              static_cast<int64_t>(at & static_cast<int>(place_mask)) * token_stride;
+            return FP8 ? e : 2 * e;
+        };
+        auto load_k = [&](int j) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const char *p = kb + offset(32 * j + 16 * s + c16, a.c.kp, a.c.kt);
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) kr[s][i] = *reinterpret_cast<const u32x4 *>(p + 64 * i + 16 * g);
+                    if constexpr (D % 64 != 0) {
+                        u32x2 x = {0u, 0u};
+                        if (64 * (D / 64) + 8 * g < D) x = *reinterpret_cast<const u32x2 *>(p + 64 * (D / 64) + 8 * g);
+                        kr[s][D / 64] = u32x4{x[0], x[1], 0u, 0u};
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::KS; ++i) {
+                        if (32 * i + 32 <= D)
+                            kr[s][i] = *reinterpret_cast<const u32x4 *>(p + 64 * i + 16 * g);
+                        else
+                            kr[s][i] = 32 * i + 8 * g < D ? *reinterpret_cast<const u32x4 *>(p + 64 * i + 16 * g)
+                                                          : u32x4{0u, 0u, 0u, 0u};
+                    }
+                }
+            }
+        };
+        auto load_v = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < C::VI; ++i) {
+                const int id = i * 64 + lane < 32 * C::NC ? i * 64 + lane : 32 * C::NC - 1;
+                const char *p = vb + offset(32 * j + id / C::NC, a.c.vp, a.c.vt);
+                vr[i] = *reinterpret_cast<const u32x4 *>(p + id % C::NC * 16);
+            }
+        };
+
+        int j = wave;
+        if (j < tiles) {
+            load_k(j);
+            load_v(j);
+        }
+        for (; j < tiles; j += 4) {
+            const bool whole = 32 * j + 32 <= left;
+            f32x4 s[QT][2];
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) s[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < C::KS; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    bf16x8 k;
+                    if constexpr (FP8)
+                        k = fp8x8_to_bf16(kr[x][i / 2][2 * (i % 2)], kr[x][i / 2][2 * (i % 2) + 1]);
+                    else
+                        k = __builtin_bit_cast(bf16x8, kr[x][i]);
+#pragma unroll
+                    for (int t = 0; t < QT; ++t) s[t][x] = mfma16x16x32(k, q[t][i], s[t][x]);
+                }
+            load_k(j + 4);
+
+            bf16x8 hi[QT], lo[QT];
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                float w[8], most = kLowest;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    w[i] = s[t][i / 4][i % 4] * to_exp2;
+                    if (!whole && 32 * j + 16 * (i / 4) + 4 * g + i % 4 >= left) w[i] = -__builtin_inff();
+                    most = fmaxf(most, w[i]);
+                }
+                if (__any(most > m[t] + 8.f)) {
+                    most = fmaxf(most, __shfl_xor(most, 16, 64));
+                    most = fmaxf(fmaxf(most, __shfl_xor(most, 32, 64)), m[t]);
+                    const float f = exp2_hw(m[t] - most);
+                    m[t] = most;
+                    l[t] *= f;
+#pragma unroll
+                    for (int i = 0; i < C::DT; ++i) o[t][i] *= f;
+                }
+                uint32_t hb[4], lb[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p0 = exp2_hw(w[2 * i] - m[t]), p1 = exp2_hw(w[2 * i + 1] - m[t]);
+                    l[t] += p0 + p1;
+                    const uint32_t u0 = __float_as_uint(p0) & 0xffff0000u, u1 = __float_as_uint(p1) & 0xffff0000u;
+                    hb[i] = (u0 >> 16) | u1;
+                    const float r0 = fmaxf(p0 - __uint_as_float(u0), 1e-37f), r1 = fmaxf(p1 - __uint_as_float(u1), 1e-37f);
+                    lb[i] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(r0), static_cast<__bf16>(r1)});
+                }
+                hi[t] = __builtin_bit_cast(bf16x8, u32x4{hb[0], hb[1], hb[2], hb[3]});
+                lo[t] = __builtin_bit_cast(bf16x8, u32x4{lb[0], lb[1], lb[2], lb[3]});
+            }
+
+#pragma unroll
+            for (int i = 0; i < C::VI; ++i) {
+                const int id = i * 64 + lane, r = id / C::NC;
+                // what lies past the sequence is zero here: its probability is too, and zero times NaN is not
+                if (!whole && 32 * j + r >= left) vr[i] = u32x4{0u, 0u, 0u, 0u};
+                if (64 * C::VI == 32 * C::NC || id < 32 * C::NC)
+                    *reinterpret_cast<u32x4 *>(vt + r * C::ROW + C::place(id % C::NC, r) * 16) = vr[i];
+            }
+            load_v(j + 4);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < C::DT; ++i) {
+                bf16x8 v;
+                if constexpr (FP8) {
+                    const int r = c16 < 8 ? 4 * g + c16 / 2 : 12 + 4 * g + c16 / 2;  // rows 16 + 4 g + (c16 / 2 - 4)
+                    const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        (__attribute__((address_space(3))) i32x2 *)(vt + r * C::ROW + C::place(i, r) * 16 + (c16 & 1) * 8));
+                    v = fp8x8_to_bf16(static_cast<uint32_t>(x[0]), static_cast<uint32_t>(x[1]));
+                } else {
+                    s16x4 x[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int r = 16 * y + 4 * g + c16 / 4, ch = 2 * i + (c16 & 3) / 2;
+                        x[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4 *)(vt + r * C::ROW + C::place(ch, r) * 16 + (c16 & 1) * 8));
+                    }
+                    v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    o[t][i] = mfma16x16x32(v, hi[t], o[t][i]);
+                    o[t][i] = mfma16x16x32(v, lo[t], o[t][i]);
+                }
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+
+    // join the waves, 16 heads at a time
+    const float nan = __builtin_nanf("");
+    float *red = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        float all = l[t];
+        all += __shfl_xor(all, 16, 64);
+        all += __shfl_xor(all, 32, 64);
+        __syncthreads();
+        if (g == 0) {
+            top[wave][c16] = m[t];
+            sum[wave][c16] = all;
+        }
+#pragma unroll
+        for (int i = 0; i < C::DT; ++i)
+            *reinterpret_cast<f32x4 *>(red + (wave * 16 + c16) * (D + 4) + 16 * i + 4 * g) = o[t][i];
+        __syncthreads();
+        for (int e = tid; e < 16 * (D / 4); e += 256) {
+            const int hq = e / (D / 4), d = e % (D / 4) * 4;
+            if (q0 + 16 * t + hq >= per) continue;
+            const float most = fmaxf(fmaxf(top[0][hq], top[1][hq]), fmaxf(top[2][hq], top[3][hq]));
+            float total = 0.f;
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = exp2_hw(top[w][hq] - most);
+                total += f * sum[w][hq];
+                v += *reinterpret_cast<const f32x4 *>(red + (w * 16 + hq) * (D + 4) + d) * f;
+            }
+            if (wrong) {
+                total = nan;
+                v = f32x4{nan, nan, nan, nan};
+            }
+            const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + q0 + 16 * t + hq;
+            if (parts > 1) {
+                float *to = a.ws + (row * a.parts + part) * (D + 4);
+                *reinterpret_cast<f32x4 *>(to + d) = v;
+                if (d == 0) *reinterpret_cast<float2 *>(to + D) = float2{most, total};
+            } else {
+                finish_head(a, row * D + d, row, d, v, most, total);
+            }
+        }
+    }
+}
+
+// Joins the parts of one sequence's head: D / 4 threads over the elements,
+// the rest over the parts.
+template <int D>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
+    constexpr int COLS = D / 4, SLICES = 256 / COLS;
+    __shared__ float red[SLICES][D + 4], peak[4];
+    const int64_t row = blockIdx.x;
+    const int parts = parts_of(a, a.lengths[row / a.q_heads]);
+    if (parts <= 1) return;  // written by its only part
+    const float *from = a.ws + row * a.parts * (D + 4);
+    const int tid = threadIdx.x;
+    float most = kLowest;
+    for (int p = tid; p < parts; p += 256) most = fmaxf(most, from[p * (D + 4) + D]);
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor(most, x, 64));
+    if ((tid & 63) == 0) peak[tid >> 6] = most;
+    __syncthreads();
+    most = fmaxf(fmaxf(peak[0], peak[1]), fmaxf(peak[2], peak[3]));
+    const int slice = tid / COLS, d = tid % COLS * 4;
+    if (slice < SLICES) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        float total = 0.f;
+        for (int p = slice; p < parts; p += SLICES) {
+            const float *x = from + static_cast<int64_t>(p) * (D + 4);
+            const float f = exp2_hw(x[D] - most);
+            v += *reinterpret_cast<const f32x4 *>(x + d) * f;
+            total += x[D + 1] * f;
+        }
+        *reinterpret_cast<f32x4 *>(&red[slice][d]) = v;
+        if (d == 0) red[slice][D] = total;
+    }
+    __syncthreads();
+    if (tid >= COLS) return;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    float total = 0.f;
+#pragma unroll
+    for (int s = 0; s < SLICES; ++s) {
+        v += *reinterpret_cast<const f32x4 *>(&red[s][d]);
+        total += red[s][D];
+    }
+    finish_head(a, row * D + d, row, d, v, most, total);
+}
+
+// Instantiated here: the launchers below are compiled for the host only.
+#define PROJ_ATTEND_INST(D)                                           \
+    template __global__ void attend_kernel<D, false, 1>(AttendArgs);  \
+    template __global__ void attend_kernel<D, true, 1>(AttendArgs);   \
+    template __global__ void attend_join_kernel<D>(AttendArgs);
+#define PROJ_ATTEND_INST2(D)                                          \
+    PROJ_ATTEND_INST(D)                                               \
+    template __global__ void attend_kernel<D, false, 2>(AttendArgs);  \
+    template __global__ void attend_kernel<D, true, 2>(AttendArgs);
+PROJ_ATTEND_INST2(64)
+PROJ_ATTEND_INST2(80)
+PROJ_ATTEND_INST2(96)
+PROJ_ATTEND_INST2(128)
+PROJ_ATTEND_INST(192)
+PROJ_ATTEND_INST(256)
+
+#ifndef __HIP_DEVICE_COMPILE__
+bool attend_dim(int dim) {
+    return dim == 64 || dim == 80 || dim == 96 || dim == 128 || dim == 192 || dim == 256;
+}
+
+template <int D>
+static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
+    // two tiles of 16 query heads to a workgroup where their outputs fit its
+    // registers; else another workgroup reads the same keys and values
+    constexpr bool kTwo = D <= 128;
+    const int per = a.q_heads / a.c.heads, qt = kTwo && per > 16 ? 2 : 1;
+    a.chunks = (per + 16 * qt - 1) / (16 * qt);
+    const int64_t rows = a.B * a.c.heads * a.chunks;
+    const int64_t span = a.window > 0 && a.window < a.max_len ? a.window : a.max_len;
+    // parts of the length: enough workgroups for four to a compute unit, none
+    // shorter than one tile for each wave nor longer than a staged chunk
+    // (lengths differ, and long parts would leave units idle at the end)
+    int64_t part = (span * rows + 4 * a.cus - 1) / (4 * a.cus);
+    part = part < 128 ? 128 : part > kChunk ? kChunk : (part + 127) / 128 * 128;
+    int64_t parts = span > part ? (span + part - 1) / part : 1;
+    const int64_t room = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
+    if (parts > 1 && parts > room) {
+        parts = room < 1 ? 1 : room;
+        part = ((span + parts - 1) / parts + 127) / 128 * 128;
+        parts = span > part ? (span + part - 1) / part : 1;
+    }
+    if (parts == 1) part = span > 0 ? span : 1;
+    a.part = part;
+    a.parts = static_cast<int>(parts);
+    const int64_t grid = rows * parts;
+    if (grid > 0x7fffffff || a.B * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
+    auto kernel = a.c.fp8 ? attend_kernel<D, true, 1> : attend_kernel<D, false, 1>;
+    if constexpr (kTwo)
+        if (qt == 2) kernel = a.c.fp8 ? attend_kernel<D, true, 2> : attend_kernel<D, false, 2>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || parts == 1) return e;
+    hipLaunchKernelGGL((attend_join_kernel<D>), dim3(static_cast<unsigned>(a.B * a.q_heads)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_attend(const AttendArgs &a, hipStream_t st) {
+    switch (a.c.dim) {
+        case 64: return launch_attend_dim<64>(a, st);
+        case 80: return launch_attend_dim<80>(a, st);
+        case 96: return launch_attend_dim<96>(a, st);
+        case 128: return launch_attend_dim<128>(a, st);
+        case 192: return launch_attend_dim<192>(a, st);
+        case 256: return launch_attend_dim<256>(a, st);
+    }
+    return hipErrorInvalidValue;
+}
+#endif
+
+}  // namespace proj

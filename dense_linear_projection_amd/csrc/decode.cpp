@@ -1,6 +1,6 @@
 // decode.cpp -- C ABI of the decoding operators (declared in
 // include/proj.h): argument checks, then one launcher each (quant.hip,
-// kvcache.hip).  None of them allocates, synchronises or tunes.
+// kvcache.hip, attend.hip).  None of them allocates, synchronises or tunes.
 #include <hip/hip_runtime.h>
 
 #include <climits>

@@ -1,5 +1,5 @@
 // decode.hpp -- launchers of the decoding operators: 4-bit weights
-// (quant.hip) and the paged key-value cache (kvcache.hip).
+// (quant.hip) and the paged key-value cache (kvcache.hip, attend.hip).
 #pragma once
 
 #include "common.hpp"
@@ -67,6 +67,10 @@ struct AttendArgs {
     float *ws;
     size_t ws_bytes;
     int cus;
+    // set by the launcher: tokens of a part, parts of the longest sequence,
+    // chunks of a key-value head's query heads
+    int64_t part = 0;
+    int parts = 0, chunks = 0;
 };
 hipError_t launch_attend(const AttendArgs &a, hipStream_t st);
 bool attend_dim(int dim);  // whether a kernel for this head size is built
