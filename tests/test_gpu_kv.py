@@ -66,6 +66,13 @@ def test_append(ctx, dtype, layout, interleaved):
         run_append(ctx, T, Hq, H, D, rot, page, dtype, layout, interleaved, 10 * i, pad=T // 5)
 
 
+@pytest.mark.parametrize("rot,interleaved", [(128, False), (64, True), (34, False), (34, True), (0, False)])
+def test_append_many_tokens(ctx, rot, interleaved):
+    """Enough tokens that a thread takes several of them, a number that does not divide evenly."""
+    for dtype, layout in ((BF16, "hnd"), (FP8, "nhd")):
+        run_append(ctx, 5003, 20, 4, 128, rot, 64, dtype, layout, interleaved, 77, pad=700)
+
+
 def test_append_ignores_places_outside(ctx):
     """Slots past the cache store nothing; positions outside the table store nothing and give NaN queries."""
     T = 9
