@@ -3,6 +3,7 @@
 //
 //     Y[m, n] = sum_g s[n, g] * (sum_{k in g} X[m, k] c[n, k] - z[n, g] sum_{k in g} X[m, k])
 #include "decode.hpp"
+#include "kernels.hpp"
 
 namespace proj {
 
@@ -39,6 +40,391 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
     if (lane == 0) {
         const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n]) : 0.f;
         store_out(a.Y, a.out, idx, apply_epilogue(acc, a.epi, b));
+    }
+}
+
+// ------------------------------------------------ on the matrix cores
+//
+// Both kernels below take K in steps of 128 and multiply X by the codes
+// themselves, in bf16 and therefore exactly: a code c becomes 16 + c, which is
+// the code's four bits put into the bf16 pattern of 16.0 (a shift and an
+// and-or for two codes), and
+//     sum_k x (c - z) = sum_k x (16 + c) - (16 + z) sum_k x
+// is had by starting the matrix product's accumulator at -(16 + z) sum_k x.
+// The sums of x come from a product with constant columns.  At a group's end
+// its fp32 sum is scaled and added: nothing is rounded below fp32.
+//
+// A lane reads 16 bytes of a column's codes: words 4 g .. 4 g + 3 of the
+// step's sixteen (g = lane / 16).  One product of 32 k takes a word from each
+// g, and which words meet in one product only matters across a group's end:
+// as loaded they are 4 g + r (r = 0..3), which is right for groups of 128;
+// exchanging rows of lanes makes it the same half of the step (groups of 64)
+// or the same quarter (groups of 32).  X is read in the same order.
+
+// An offset past every resource made here (they are below 2^31 bytes): a load there gives zero.
+constexpr uint32_t kOutside = 0xffffff00u;
+
+// Which of a step's sixteen words (and chunks of 8 x) lane group g holds in register r.
+template <int GROUP>
+__device__ __forceinline__ int word_of(int r, int g) {
+    if (GROUP == 128) return 4 * g + r;
+    if (GROUP == 64) return (r & 1) + 8 * (r >> 1) + 4 * (g & 1) + 2 * (g >> 1);
+    return 4 * r + g;
+}
+
+template <int GROUP>
+__device__ __forceinline__ u32x4 arrange(u32x4 w) {
+    if constexpr (GROUP <= 64) {
+        const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+        w = u32x4{a[0], b[0], a[1], b[1]};
+        if constexpr (GROUP == 32) {
+            const auto c = __builtin_amdgcn_permlane16_swap(w[0], w[1], false, false);
+            const auto d = __builtin_amdgcn_permlane16_swap(w[2], w[3], false, false);
+            w = u32x4{c[0], c[1], d[0], d[1]};
+        }
+    }
+    return w;
+}
+
+// Eight codes -> 16 + code in bf16.
+__device__ __forceinline__ bf16x8 widen(uint32_t w) {
+    const uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+    return __builtin_bit_cast(bf16x8, u32x4{((w << 3) & mask) | sixteen, ((w >> 1) & mask) | sixteen,
+                                            ((w >> 5) & mask) | sixteen, ((w >> 9) & mask) | sixteen});
+}
+
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0);
+}
+
+// Words 4 g .. 4 g + 3 of a step of one column; past the resource's end zero.
+// VEC: K is a multiple of 32, so that no load straddles that end.
+template <bool VEC>
+__device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    if constexpr (VEC) {
+        return buffer_load16(r, off);
+    } else {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(off + 4 * i), 0, 0);
+        return w;
+    }
+}
+
+// Up to 16 token rows: bound by reading the codes once, and at the smallest
+// sizes by the latency of doing so.  A workgroup owns 16 * NT columns; its
+// waves take steps in turn (two neighbouring ones at a time where there are
+// enough: 128 contiguous bytes of a column), straight from memory into
+// registers with DEPTH steps in flight and no barrier, and add up through LDS
+// at the end.  Nothing is split over workgroups, so there is one launch and no
+// workspace.  The columns' scales lie in LDS as fp32, staged `span` steps at
+// a time.
+template <int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
+__global__ __launch_bounds__(WAVES * 64) void quant_few_kernel(QuantArgs a, int span) {
+    constexpr int GP = 128 / GROUP, PER = 4 / GP;  // groups of a step, registers of a group
+    constexpr int COLS = 16 * NT, THREADS = WAVES * 64;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * COLS;
+    const int cols = a.N - n0 < COLS ? static_cast<int>(a.N - n0) : COLS;
+    const int M = static_cast<int>(a.M), steps = static_cast<int>((a.K + 127) / 128);
+    const uint32_t words = static_cast<uint32_t>(a.K / 8);
+    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.codes + n0 * words, static_cast<uint32_t>(cols) * words * 4u);
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X, static_cast<uint32_t>(M) * words * 16u);
+
+    f32x4 acc[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{0xbf80bf80u, 0xbf80bf80u, 0xbf80bf80u, 0xbf80bf80u});
+
+    for (int from = 0; from < steps; from += span) {
+        const int count = steps - from < span ? steps - from : span;
+        const int pair = count >= 4 * WAVES ? 1 : 0;
+        auto step_of = [&](int i) { return ((wave + WAVES * (i >> pair)) << pair) + (i & pair); };
+        u32x4 w[DEPTH][NT], x[DEPTH][4];
+        auto fetch = [&](int slot, int i) {
+            const int at = step_of(i);
+            const bool live = at < count;
+            const uint32_t word = static_cast<uint32_t>(from + at) * 16u;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                w[slot][t] = load_words<VEC>(rw, live ? ((16u * t + c16) * words + word + 4u * g) * 4u : kOutside);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t k = word + word_of<GROUP>(r, g);
+                x[slot][r] = buffer_load16(rx, live && c16 < M && k < words ? (c16 * words + k) * 16u : kOutside);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) fetch(i, i);
+
+        // scales [column][group], rows an odd number of floats apart; behind them 16 + zero
+        const int groups = count * GP, row = groups | 1;
+        float *sc = reinterpret_cast<float *>(lds);
+        float *zc = sc + COLS * row;
+        if (from > 0) __syncthreads();
+        for (int n = wave; n < COLS; n += WAVES)
+            for (int i = lane; i < groups; i += 64) {
+                const int64_t at = from * GP + i;
+                const bool ok = n < cols && at < a.G;
+                sc[n * row + i] = ok ? group_scale(a, (n0 + n) * a.G + at) : 0.f;
+                if (a.zeros) zc[n * row + i] = ok ? 16.f + static_cast<float>(a.zeros[(n0 + n) * a.G + at]) : 0.f;
+            }
+        __syncthreads();
+
+        for (int i0 = 0; step_of(i0) < count; i0 += DEPTH) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                const int at = step_of(i0 + d);
+                if (at >= count) break;
+                bf16x8 xv[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) xv[r] = __builtin_bit_cast(bf16x8, x[d][r]);
+                f32x4 minus_x[GP];
+#pragma unroll
+                for (int q = 0; q < GP; ++q) {
+                    minus_x[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int r = q * PER; r < (q + 1) * PER; ++r) minus_x[q] = mfma16x16x32(xv[r], minus, minus_x[q]);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const u32x4 wt = arrange<GROUP>(w[d][t]);
+#pragma unroll
+                    for (int q = 0; q < GP; ++q) {
+                        const int si = (16 * t + c16) * row + at * GP + q;
+                        const float s = sc[si], z = a.zeros ? zc[si] : 24.f;
+                        f32x4 p = minus_x[q] * z;
+#pragma unroll
+                        for (int r = q * PER; r < (q + 1) * PER; ++r) p = mfma16x16x32(xv[r], widen(wt[r]), p);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(s, p[v], acc[t][v]);
+                    }
+                }
+                fetch(d, i0 + d + DEPTH);
+            }
+        }
+    }
+
+    // add the waves' sums; entry (row m, column n) at m * COLS + n
+    __syncthreads();
+    float *red = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * g + v) * COLS + 16 * t + c16] = acc[t][v];
+    __syncthreads();
+    for (int e = tid; e < M * COLS; e += THREADS) {
+        const int m = e / COLS, n = e % COLS;
+        if (n >= cols) continue;
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) y += red[(i * 16 + m) * COLS + n];
+        const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n0 + n]) : 0.f;
+        store_out(a.Y, a.out, m * a.N + n0 + n, apply_epilogue(y, a.epi, b));
+    }
+}
+
+template <int MT, int NT, int WM, int WN, int GROUP>
+struct TileCfg {
+    static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = WM * WN;
+    static constexpr int GP = 128 / GROUP, PER = 4 / GP;
+    static constexpr int RING = 4;                      // stages of X in LDS
+    static constexpr int STAGE = BM * 256;              // bytes of one
+    static constexpr int NX = STAGE / 1024 / WAVES;     // copies of a wave
+    static constexpr int SI = (BN * GP + WAVES * 64 - 1) / (WAVES * 64);  // scales of a thread
+    static constexpr int SCALES = GP * BN;              // float2 each
+    static constexpr int SUMS = GP * BM;                // floats
+    static constexpr int LDS = RING * STAGE + 2 * (SCALES * 8 + SUMS * 4);
+    static_assert(STAGE % (1024 * WAVES) == 0, "copies divide evenly over the waves");
+};
+
+// More rows: tiles of BM rows by BN columns, 16 MT x 16 NT to a wave.  X
+// goes through a ring of four steps in LDS, filled by copies that pass no
+// register (16-byte chunk c of row m at c ^ m % 16, so that the 16 rows of a
+// fragment fall on different banks); codes go from memory into the registers
+// of the waves that use them, one step ahead, and are widened there.  In step
+// s the workgroup multiplies step s, adds up the x of step s + 1 (one 16-row
+// tile to a wave), puts down the scales of s + 1 and fetches those of s + 2
+// and X of s + 3; one barrier a step publishes all of it.
+template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool VEC>
+__global__ __launch_bounds__(WM *WN * 64) void quant_tile_kernel(QuantArgs a, int splits) {
+    using C = TileCfg<MT, NT, WM, WN, GROUP>;
+    constexpr int GP = C::GP, PER = C::PER, THREADS = C::WAVES * 64;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    float2 *sc = reinterpret_cast<float2 *>(lds + C::RING * C::STAGE);
+    float *sums = reinterpret_cast<float *>(lds + C::RING * C::STAGE + 2 * C::SCALES * 8);
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WM, wn = wave / WM;
+
+    // Workgroup ids go round the eight dies in turn; each die takes a
+    // contiguous run of tiles, rows fastest, so that the codes of a column
+    // block are fetched by one die.
+    const uint32_t mb = static_cast<uint32_t>((a.M + C::BM - 1) / C::BM), total = gridDim.x;
+    const uint32_t die = blockIdx.x % 8, share = total / 8, more = total % 8;
+    uint32_t id = die * share + (die < more ? die : more) + blockIdx.x / 8;
+    const int split = static_cast<int>(id % static_cast<uint32_t>(splits));
+    id /= static_cast<uint32_t>(splits);
+    const int64_t m0 = static_cast<int64_t>(id % mb) * C::BM, n0 = static_cast<int64_t>(id / mb) * C::BN;
+    const int rows = a.M - m0 < C::BM ? static_cast<int>(a.M - m0) : C::BM;
+    const int cols = a.N - n0 < C::BN ? static_cast<int>(a.N - n0) : C::BN;
+    const int steps = static_cast<int>((a.K + 127) / 128);
+    const int first = static_cast<int>(static_cast<int64_t>(steps) * split / splits);
+    const int count = static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / splits) - first;
+    const uint32_t words = static_cast<uint32_t>(a.K / 8);
+    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.codes + n0 * words, static_cast<uint32_t>(cols) * words * 4u);
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X + m0 * a.K, static_cast<uint32_t>(rows) * words * 16u);
+
+    // copies: block j * WAVES + wave of a stage is four rows of 16 chunks; lane's row and chunk
+    const int copy_row = lane / 16;
+    auto copy_x = [&](int s) {
+        char *slot = lds + (s % C::RING) * C::STAGE;
+        const uint32_t word = static_cast<uint32_t>(first + s) * 16u;
+#pragma unroll
+        for (int j = 0; j < C::NX; ++j) {
+            const int r = (j * C::WAVES + wave) * 4 + copy_row;
+            const uint32_t k = word + static_cast<uint32_t>(c16 ^ (r & 15));
+            const bool ok = s < count && r < rows && k < words;
+            dma16_buf(rx, ok ? (static_cast<uint32_t>(r) * words + k) * 16u : kOutside, 0, slot + (j * C::WAVES + wave) * 1024);
+        }
+    };
+    u32x4 w[NT];
+    auto load_w = [&](int s) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const uint32_t col = static_cast<uint32_t>((wn * NT + t) * 16 + c16);
+            w[t] = load_words<VEC>(rw, s < count ? (col * words + static_cast<uint32_t>(first + s) * 16u + 4u * g) * 4u : kOutside);
+        }
+    };
+    float sv[C::SI], zv[C::SI];
+    auto load_scales = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < C::SI; ++i) {
+            const int e = i * THREADS + tid, col = e / GP;
+            const int64_t at = static_cast<int64_t>(first + s) * GP + e % GP;
+            sv[i] = 0.f;
+            zv[i] = 0.f;
+            if (s < count && col < cols && at < a.G) {
+                sv[i] = group_scale(a, (n0 + col) * a.G + at);
+                zv[i] = ZEROS ? 16.f + static_cast<float>(a.zeros[(n0 + col) * a.G + at]) : 0.f;
+            }
+        }
+    };
+    auto put_scales = [&](int s) {
+        float2 *to = sc + (s & 1) * C::SCALES;
+#pragma unroll
+        for (int i = 0; i < C::SI; ++i) {
+            const int e = i * THREADS + tid;
+            if (e < C::SCALES) to[e % GP * C::BN + e / GP] = float2{sv[i], zv[i]};
+        }
+    };
+    auto fragment = [&](const char *slot, int row, int r) {
+        return *reinterpret_cast<const bf16x8 *>(slot + row * 256 + ((word_of<GROUP>(r, g) ^ (row & 15)) << 4));
+    };
+    // -sum x (times 24, 16 and the zero point of 8, where there are no zeros given) of a step's groups
+    const uint32_t unit = ZEROS ? 0xbf80bf80u : 0xc1c0c1c0u;
+    const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{unit, unit, unit, unit});
+    auto add_x = [&](int s) {
+        const char *slot = lds + (s % C::RING) * C::STAGE;
+        for (int t = wave; t < C::BM / 16; t += C::WAVES)
+#pragma unroll
+            for (int q = 0; q < GP; ++q) {
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int r = q * PER; r < (q + 1) * PER; ++r) v = mfma16x16x32(fragment(slot, 16 * t + c16, r), minus, v);
+                if (c16 == 0) *reinterpret_cast<f32x4 *>(sums + (s & 1) * C::SUMS + q * C::BM + 16 * t + 4 * g) = v;
+            }
+    };
+
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // Per step a wave issues NX copies, then its loads of codes (NW); waiting
+    // until that many are left therefore leaves the copies of two steps ahead
+    // in flight and has those of the next one done.
+    constexpr int NW = VEC ? NT : 4 * NT;
+    load_scales(0);
+    copy_x(0);
+    copy_x(1);
+    put_scales(0);
+    load_scales(1);
+    copy_x(2);
+    load_w(0);
+    wait_vm<2 * C::NX + NW>();
+    __syncthreads();
+    add_x(0);
+
+    for (int s = 0; s < count; ++s) {
+        wait_vm<C::NX + NW>();
+        lds_wait_all();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        copy_x(s + 3);
+        u32x4 wc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) wc[t] = arrange<GROUP>(w[t]);
+        load_w(s + 1);
+        put_scales(s + 1);
+        load_scales(s + 2);
+        add_x(s + 1);
+
+        const char *slot = lds + (s % C::RING) * C::STAGE;
+        const float2 *scs = sc + (s & 1) * C::SCALES + wn * NT * 16 + c16;
+        const float *xs = sums + (s & 1) * C::SUMS + wm * MT * 16 + 4 * g;
+#pragma unroll
+        for (int q = 0; q < GP; ++q) {
+            bf16x8 xf[MT][PER];
+            f32x4 cs[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                cs[i] = *reinterpret_cast<const f32x4 *>(xs + q * C::BM + 16 * i);
+#pragma unroll
+                for (int r = 0; r < PER; ++r) xf[i][r] = fragment(slot, (wm * MT + i) * 16 + c16, q * PER + r);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const float2 sz = scs[q * C::BN + 16 * t];
+                f32x4 p[MT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) p[i] = ZEROS ? cs[i] * sz.y : cs[i];
+#pragma unroll
+                for (int r = 0; r < PER; ++r) {
+                    const bf16x8 wf = widen(wc[t][q * PER + r]);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) p[i] = mfma16x16x32(xf[i][r], wf, p[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[i][t][v] = __builtin_fmaf(sz.x, p[i][v], acc[i][t][v]);
+            }
+        }
+    }
+    wait_vm<0>();
+
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int col = (wn * NT + t) * 16 + c16;
+        if (col >= cols) continue;
+        const float b = (a.epi & 1) && splits == 1 ? bf16_bits_to_f32(a.bias[n0 + col]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int r = (wm * MT + i) * 16 + 4 * g + v;
+                if (r >= rows) continue;
+                const int64_t at = (m0 + r) * a.N + n0 + col;
+                if (splits > 1)
+                    a.ws[split * a.M * a.N + at] = acc[i][t][v];
+                else
+                    store_out(a.Y, a.out, at, apply_epilogue(acc[i][t][v], a.epi, b));
+            }
     }
 }
 
@@ -92,6 +478,26 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
     codes[(n * K + k) / 8] = word;
 }
 
+// Instantiated here: the launchers below are compiled for the host only.
+#define PROJ_QUANT_FEW(G, V)                                                                \
+    template __global__ void quant_few_kernel<1, 8, 4, G, V>(QuantArgs, int);               \
+    template __global__ void quant_few_kernel<2, 8, 3, G, V>(QuantArgs, int);               \
+    template __global__ void quant_few_kernel<4, 4, 3, G, V>(QuantArgs, int);
+#define PROJ_QUANT_TILE(G, Z, V)                                                            \
+    template __global__ void quant_tile_kernel<2, 2, 1, 4, G, Z, V>(QuantArgs, int);        \
+    template __global__ void quant_tile_kernel<4, 2, 1, 4, G, Z, V>(QuantArgs, int);        \
+    template __global__ void quant_tile_kernel<4, 4, 2, 4, G, Z, V>(QuantArgs, int);
+#define PROJ_QUANT_GROUP(G)      \
+    PROJ_QUANT_FEW(G, true)      \
+    PROJ_QUANT_FEW(G, false)     \
+    PROJ_QUANT_TILE(G, true, true)   \
+    PROJ_QUANT_TILE(G, true, false)  \
+    PROJ_QUANT_TILE(G, false, true)  \
+    PROJ_QUANT_TILE(G, false, false)
+PROJ_QUANT_GROUP(32)
+PROJ_QUANT_GROUP(64)
+PROJ_QUANT_GROUP(128)
+
 #ifndef __HIP_DEVICE_COMPILE__
 static bool grid_for(int64_t items, int64_t per, unsigned *grid) {
     const int64_t g = (items + per - 1) / per;
@@ -100,7 +506,83 @@ static bool grid_for(int64_t items, int64_t per, unsigned *grid) {
     return true;
 }
 
+template <int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
+static hipError_t run_few(const QuantArgs &a, hipStream_t st) {
+    unsigned grid;
+    if (!grid_for(a.N, 16 * NT, &grid)) return hipErrorInvalidConfiguration;
+    constexpr int gp = 128 / GROUP, most = 64 << 10;
+    // as many steps' scales as 64 KB hold
+    const int64_t steps = (a.K + 127) / 128;
+    const int per = a.zeros ? 8 : 4;
+    int64_t span = (most / (16 * NT * per) - 1) / gp;
+    if (span > steps) span = steps;
+    const int64_t row = span * gp | 1;
+    int64_t lds = 16 * NT * row * per;
+    if (lds < WAVES * 1024 * NT) lds = WAVES * 1024 * NT;
+    hipLaunchKernelGGL((quant_few_kernel<NT, WAVES, DEPTH, GROUP, VEC>), dim3(grid), dim3(WAVES * 64),
+                       static_cast<unsigned>(lds), st, a, static_cast<int>(span));
+    return hipGetLastError();
+}
+
+template <int GROUP, bool VEC>
+static hipError_t launch_few(const QuantArgs &a, hipStream_t st) {
+    if (a.N <= 16 * static_cast<int64_t>(a.cus)) return run_few<1, 8, 4, GROUP, VEC>(a, st);
+    if (a.N <= 64 * static_cast<int64_t>(a.cus)) return run_few<2, 8, 3, GROUP, VEC>(a, st);
+    return run_few<4, 4, 3, GROUP, VEC>(a, st);
+}
+
+template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool VEC>
+static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
+    using C = TileCfg<MT, NT, WM, WN, GROUP>;
+    const int64_t tiles = ((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN), steps = (a.K + 127) / 128;
+    // split K where the tiles leave compute units idle, in runs of four steps at least
+    int64_t splits = tiles >= a.cus ? 1 : 2 * a.cus / tiles;
+    if (splits > steps / 4) splits = steps / 4;
+    const int64_t room = static_cast<int64_t>(a.ws_bytes / 4) / (a.M * a.N);
+    if (splits > room) splits = room;
+    if (splits < 1) splits = 1;
+    if (tiles * splits > 0x7fffffff) return hipErrorInvalidConfiguration;
+    auto kernel = quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, VEC>;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::LDS);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles * splits)), dim3(C::WAVES * 64), C::LDS, st, a,
+                       static_cast<int>(splits));
+    e = hipGetLastError();
+    if (e != hipSuccess || splits == 1) return e;
+    Args r{};
+    r.M = a.M, r.N = a.N, r.K = a.K;
+    r.epi = a.epi, r.out = a.out;
+    r.bias = a.bias;
+    r.Y = a.Y;
+    r.ws = a.ws;
+    return launch_splitk_reduce(r, static_cast<int>(splits), st);
+}
+
+template <int GROUP, bool ZEROS, bool VEC>
+static hipError_t launch_tile(const QuantArgs &a, hipStream_t st) {
+    if (a.M <= 32) return run_tile<2, 2, 1, 4, GROUP, ZEROS, VEC>(a, st);
+    if (((a.M + 127) / 128) * ((a.N + 255) / 256) * 2 > a.cus) return run_tile<4, 4, 2, 4, GROUP, ZEROS, VEC>(a, st);
+    return run_tile<4, 2, 1, 4, GROUP, ZEROS, VEC>(a, st);
+}
+
+template <int GROUP, bool VEC>
+static hipError_t launch_group(const QuantArgs &a, hipStream_t st) {
+    if (a.M <= 16) return launch_few<GROUP, VEC>(a, st);
+    return a.zeros ? launch_tile<GROUP, true, VEC>(a, st) : launch_tile<GROUP, false, VEC>(a, st);
+}
+
 hipError_t launch_quant(const QuantArgs &a, hipStream_t st) {
+    // the matrix-core kernels read X in 16-byte chunks, and address a tile's
+    // codes (at most 256 columns) and rows of X (128) with 32 bits
+    if (a.K > 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.K < (int64_t{1} << 23)) {
+        const bool vec = a.K % 32 == 0;
+        switch (a.group) {
+            case 32: return vec ? launch_group<32, true>(a, st) : launch_group<32, false>(a, st);
+            case 64: return vec ? launch_group<64, true>(a, st) : launch_group<64, false>(a, st);
+            case 128: return vec ? launch_group<128, true>(a, st) : launch_group<128, false>(a, st);
+        }
+    }
     unsigned grid;
     if (!grid_for(a.M * a.N, 4, &grid)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(quant_rows_kernel, dim3(grid), dim3(256), 0, st, a);

@@ -286,7 +286,7 @@ proj_status proj_quantize_weights(proj_ctx *ctx, const void *W, int64_t N, int64
  * Epilogue, output types, M = 0, N = 0, K = 0 and overlap rules as proj_run.
  * Products of X with the codes are exact, sums are fp32, the scales are
  * applied to the fp32 sums of a group: nothing is rounded to bf16 before the
- * output.  Allocates nothing and never synchronises, so it may be captured;
+ * output.  A NaN or an infinity in X makes its row's results NaN.  Allocates nothing and never synchronises, so it may be captured;
  * which kernel runs follows from sizes and alignment alone (no tuning, no
  * plan), so the same call gives the same bits every time.  Codes that are not
  * 4-byte aligned, scales or X not aligned to their type: PROJ_ERR_INVALID_ARG. */
