@@ -128,6 +128,12 @@ __device__ __forceinline__ void dma16_buf(__amdgpu_buffer_rsrc_t r, uint32_t vof
                                              voff, soff, 0, 0);
 }
 
+// The same copy of 4 bytes a lane.
+__device__ __forceinline__ void dma4_buf(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void *lds_wave_base) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds_wave_base, 4,
+                                             voff, soff, 0, 0);
+}
+
 // The same copy with the non-temporal (streaming) cache hint.
 __device__ __forceinline__ void dma16_buf_nt(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
                                              void *lds_wave_base) {

@@ -2,6 +2,8 @@
 // layout and making of such weights.
 //
 //     Y[m, n] = sum_g s[n, g] * (sum_{k in g} X[m, k] c[n, k] - z[n, g] sum_{k in g} X[m, k])
+#include <type_traits>
+
 #include "decode.hpp"
 #include "kernels.hpp"
 
@@ -87,12 +89,20 @@ __device__ __forceinline__ u32x4 arrange(u32x4 w) {
     return w;
 }
 
-// Eight codes -> 16 + code in bf16.
-__device__ __forceinline__ bf16x8 widen(uint32_t w) {
-    const uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
-    return __builtin_bit_cast(bf16x8, u32x4{((w << 3) & mask) | sixteen, ((w >> 1) & mask) | sixteen,
-                                            ((w >> 5) & mask) | sixteen, ((w >> 9) & mask) | sixteen});
-}
+// Eight codes -> 16 + code in bf16.  The two constants are kept in registers
+// (their values hidden from the compiler) so that and-then-or is one
+// instruction, which takes no literal: 8 instructions a word instead of 12.
+struct Widen {
+    uint32_t mask, sixteen;
+    __device__ __forceinline__ Widen() {
+        asm("s_mov_b32 %0, 0x00780078" : "=s"(mask));
+        asm("v_mov_b32 %0, 0x41804180" : "=v"(sixteen));
+    }
+    __device__ __forceinline__ bf16x8 operator()(uint32_t w) const {
+        return __builtin_bit_cast(bf16x8, u32x4{((w << 3) & mask) | sixteen, ((w >> 1) & mask) | sixteen,
+                                                ((w >> 5) & mask) | sixteen, ((w >> 9) & mask) | sixteen});
+    }
+};
 
 __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0);
@@ -101,14 +111,14 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_
 // Words 4 g .. 4 g + 3 of a step of one column; past the resource's end zero.
 // VEC: K is a multiple of 32, so that no load straddles that end.
 template <bool VEC>
-__device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+__device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step = 0) {
     if constexpr (VEC) {
-        return buffer_load16(r, off);
+        return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), static_cast<int>(step), 0);
     } else {
         u32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(off + 4 * i), 0, 0);
+            w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(off + 4 * i), static_cast<int>(step), 0);
         return w;
     }
 }
@@ -135,6 +145,7 @@ __global__ __launch_bounds__(WAVES * 64) void quant_few_kernel(QuantArgs a, int 
     const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.codes + n0 * words, static_cast<uint32_t>(cols) * words * 4u);
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X, static_cast<uint32_t>(M) * words * 16u);
 
+    const Widen widen;
     f32x4 acc[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -232,31 +243,36 @@ template <int MT, int NT, int WM, int WN, int GROUP>
 struct TileCfg {
     static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, WAVES = WM * WN;
     static constexpr int GP = 128 / GROUP, PER = 4 / GP;
-    static constexpr int RING = 4;                      // stages of X in LDS
-    static constexpr int STAGE = BM * 256;              // bytes of one
+    static constexpr int RING = 3;                      // steps in LDS
+    static constexpr int STAGE = BM * 256;              // bytes of a step's X
     static constexpr int NX = STAGE / 1024 / WAVES;     // copies of a wave
+    static constexpr int WSTAGE = BN * 64;              // bytes of a step's codes
+    static constexpr int NW = WSTAGE / 1024 / WAVES;    // copies of a wave
     static constexpr int SI = (BN * GP + WAVES * 64 - 1) / (WAVES * 64);  // scales of a thread
     static constexpr int SCALES = GP * BN;              // float2 each
     static constexpr int SUMS = GP * BM;                // floats
-    static constexpr int LDS = RING * STAGE + 2 * (SCALES * 8 + SUMS * 4);
-    static_assert(STAGE % (1024 * WAVES) == 0, "copies divide evenly over the waves");
+    static constexpr int LDS = RING * (STAGE + WSTAGE) + 2 * (SCALES * 8 + SUMS * 4);
+    static_assert(STAGE % (1024 * WAVES) == 0 && WSTAGE % (1024 * WAVES) == 0, "copies divide evenly over the waves");
 };
 
-// More rows: tiles of BM rows by BN columns, 16 MT x 16 NT to a wave.  X
-// goes through a ring of four steps in LDS, filled by copies that pass no
-// register (16-byte chunk c of row m at c ^ m % 16, so that the 16 rows of a
-// fragment fall on different banks); codes go from memory into the registers
-// of the waves that use them, one step ahead, and are widened there.  In step
-// s the workgroup multiplies step s, adds up the x of step s + 1 (one 16-row
-// tile to a wave), puts down the scales of s + 1 and fetches those of s + 2
-// and X of s + 3; one barrier a step publishes all of it.
+// More rows: tiles of BM rows by BN columns, 16 MT x 16 NT to a wave.  X and
+// the codes go through rings of three steps in LDS, filled by copies that pass
+// no register (16-byte chunk c of X's row m at c ^ m % 16, so that the 16 rows
+// of a fragment fall on different banks); codes are widened in the registers
+// of the waves that use them.  In step s the workgroup multiplies step s,
+// adds up the x of step s + 1 (one 16-row tile to a wave), puts down the scales
+// of s + 1, reads its X fragments of s + 1, and fetches the codes of s + 2 and
+// the scales and X of s + 3; one barrier a step publishes all of it.  Loads
+// complete in order, so whatever is used a step after its issue makes all that
+// was issued before it wait: everything is used two steps after.
 template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool VEC>
-__global__ __launch_bounds__(WM *WN * 64) void quant_tile_kernel(QuantArgs a, int splits) {
+__global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a, int splits) {
     using C = TileCfg<MT, NT, WM, WN, GROUP>;
     constexpr int GP = C::GP, PER = C::PER, THREADS = C::WAVES * 64;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    float2 *sc = reinterpret_cast<float2 *>(lds + C::RING * C::STAGE);
-    float *sums = reinterpret_cast<float *>(lds + C::RING * C::STAGE + 2 * C::SCALES * 8);
+    char *wlds = lds + C::RING * C::STAGE;
+    float2 *sc = reinterpret_cast<float2 *>(wlds + C::RING * C::WSTAGE);
+    float *sums = reinterpret_cast<float *>(sc + 2 * C::SCALES);
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WM, wn = wave / WM;
 
@@ -275,118 +291,180 @@ __global__ __launch_bounds__(WM *WN * 64) void quant_tile_kernel(QuantArgs a, in
     const int first = static_cast<int>(static_cast<int64_t>(steps) * split / splits);
     const int count = static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / splits) - first;
     const uint32_t words = static_cast<uint32_t>(a.K / 8);
-    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.codes + n0 * words, static_cast<uint32_t>(cols) * words * 4u);
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X + m0 * a.K, static_cast<uint32_t>(rows) * words * 16u);
 
-    // copies: block j * WAVES + wave of a stage is four rows of 16 chunks; lane's row and chunk
-    const int copy_row = lane / 16;
-    auto copy_x = [&](int s) {
-        char *slot = lds + (s % C::RING) * C::STAGE;
+    // Byte offsets of a lane's copies of X (block j * WAVES + wave of a stage is
+    // four rows of 16 chunks), codes and scales.  Rows and columns past the
+    // end lie outside the resources; steps past the end (which are issued all
+    // the same, so that every step waits for the same count) use empty ones.
+    // A step moves a scalar offset, which the bounds may not include: only in
+    // a row's last step, if it is short, do lanes work out theirs.
+    const uint32_t xbytes = static_cast<uint32_t>(rows) * words * 16u, wbytes = static_cast<uint32_t>(cols) * words * 4u;
+    const uint32_t G = static_cast<uint32_t>(a.G), sbytes = static_cast<uint32_t>(cols) * G;
+    const uint32_t size = a.scales_f32 ? 4 : 2;
+    const char *scale0 = static_cast<const char *>(a.scales) + n0 * a.G * size;
+    const uint8_t *zero0 = ZEROS ? a.zeros + n0 * a.G : nullptr;
+    uint32_t xoff[C::NX], woff[C::NW], soff[C::SI];
+#pragma unroll
+    for (int j = 0; j < C::NX; ++j) {
+        const uint32_t r = static_cast<uint32_t>((j * C::WAVES + wave) * 4 + lane / 16);
+        xoff[j] = (r * words + (static_cast<uint32_t>(c16) ^ (r & 15))) * 16u;
+    }
+#pragma unroll
+    for (int j = 0; j < C::NW; ++j)
+        woff[j] = (static_cast<uint32_t>((j * C::WAVES + wave) * 16 + lane / 4) * words + lane % 4 * 4u) * 4u;
+#pragma unroll
+    for (int i = 0; i < C::SI; ++i) {
+        const uint32_t e = i * THREADS + tid;
+        soff[i] = e / GP * G + e % GP;
+    }
+    auto copy_x = [&](int s, int j) {
+        char *to = lds + (s % C::RING) * C::STAGE + (j * C::WAVES + wave) * 1024;
+        const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.X + m0 * a.K, s < count ? xbytes : 0u);
         const uint32_t word = static_cast<uint32_t>(first + s) * 16u;
-#pragma unroll
-        for (int j = 0; j < C::NX; ++j) {
-            const int r = (j * C::WAVES + wave) * 4 + copy_row;
-            const uint32_t k = word + static_cast<uint32_t>(c16 ^ (r & 15));
-            const bool ok = s < count && r < rows && k < words;
-            dma16_buf(rx, ok ? (static_cast<uint32_t>(r) * words + k) * 16u : kOutside, 0, slot + (j * C::WAVES + wave) * 1024);
+        if (word + 16 <= words) {
+            dma16_buf(r, xoff[j], word * 16u, to);
+        } else {
+            const uint32_t row = static_cast<uint32_t>((j * C::WAVES + wave) * 4 + lane / 16);
+            const bool in = word + (static_cast<uint32_t>(c16) ^ (row & 15)) < words;  // past the row: zeros
+            dma16_buf(r, in ? xoff[j] + word * 16u : kOutside, 0, to);
         }
     };
-    u32x4 w[NT];
-    auto load_w = [&](int s) {
+    // codes: block j * WAVES + wave of a step is 16 columns of 64 bytes
+    auto copy_w = [&](int s, int j) {
+        char *to = wlds + (s % C::RING) * C::WSTAGE + (j * C::WAVES + wave) * 1024;
+        const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.codes + n0 * words, s < count ? wbytes : 0u);
+        const uint32_t word = static_cast<uint32_t>(first + s) * 16u;
+        if constexpr (VEC) {
+            const bool inside = word + 16 <= words;
+            dma16_buf(r, woff[j] + (inside ? 0u : word * 4u), inside ? word * 4u : 0u, to);
+        } else {
+            // four bytes to a lane, so that none straddles the resource's end
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const uint32_t col = static_cast<uint32_t>((wn * NT + t) * 16 + c16);
-            w[t] = load_words<VEC>(rw, s < count ? (col * words + static_cast<uint32_t>(first + s) * 16u + 4u * g) * 4u : kOutside);
-        }
-    };
-    float sv[C::SI], zv[C::SI];
-    auto load_scales = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < C::SI; ++i) {
-            const int e = i * THREADS + tid, col = e / GP;
-            const int64_t at = static_cast<int64_t>(first + s) * GP + e % GP;
-            sv[i] = 0.f;
-            zv[i] = 0.f;
-            if (s < count && col < cols && at < a.G) {
-                sv[i] = group_scale(a, (n0 + col) * a.G + at);
-                zv[i] = ZEROS ? 16.f + static_cast<float>(a.zeros[(n0 + col) * a.G + at]) : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t col = (j * C::WAVES + wave) * 16u + 4u * i + lane / 16;
+                dma4_buf(r, (col * words + word + c16) * 4u, 0, to + i * 256);
             }
         }
     };
-    auto put_scales = [&](int s) {
+    // scales and zero points as they are in memory: converting them waits for them
+    uint32_t sv[2][C::SI], zv[2][C::SI];
+    auto load_scales = [&](int s, int odd) {
+        const uint32_t at = static_cast<uint32_t>(first + s) * GP;
+        const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(scale0, s < count ? sbytes * size : 0u);
+        const __amdgpu_buffer_rsrc_t rz = buffer_rsrc(zero0, s < count ? sbytes : 0u);
+#pragma unroll
+        for (int i = 0; i < C::SI; ++i) {
+            const uint32_t e = i * THREADS + tid;
+            const uint32_t off = GP == 1 || at + e % GP < G ? soff[i] + at : kOutside / 4;
+            if (a.scales_f32)
+                sv[odd][i] = __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(off * 4u), 0, 0);
+            else
+                sv[odd][i] = __builtin_amdgcn_raw_buffer_load_b16(rs, static_cast<int>(off * 2u), 0, 0);
+            if (ZEROS) zv[odd][i] = __builtin_amdgcn_raw_buffer_load_b8(rz, static_cast<int>(off), 0, 0);
+        }
+    };
+    auto put_scales = [&](int s, int odd) {
         float2 *to = sc + (s & 1) * C::SCALES;
 #pragma unroll
         for (int i = 0; i < C::SI; ++i) {
             const int e = i * THREADS + tid;
-            if (e < C::SCALES) to[e % GP * C::BN + e / GP] = float2{sv[i], zv[i]};
+            const float scale = __uint_as_float(a.scales_f32 ? sv[odd][i] : sv[odd][i] << 16);
+            const float zero = ZEROS ? 16.f + static_cast<float>(zv[odd][i]) : 0.f;
+            if (e < C::SCALES) to[e % GP * C::BN + e / GP] = float2{scale, zero};
         }
     };
-    auto fragment = [&](const char *slot, int row, int r) {
-        return *reinterpret_cast<const bf16x8 *>(slot + row * 256 + ((word_of<GROUP>(r, g) ^ (row & 15)) << 4));
+    // LDS offsets of a lane's fragments within a 16-row tile
+    int xaddr[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) xaddr[r] = c16 * 256 + ((word_of<GROUP>(r, g) ^ c16) << 4);
+    auto fragment = [&](int s, int tile, int r) {
+        return *reinterpret_cast<const bf16x8 *>(lds + (s % C::RING) * C::STAGE + tile * 4096 + xaddr[r]);
     };
-    // -sum x (times 24, 16 and the zero point of 8, where there are no zeros given) of a step's groups
+    // -sum x (times 24, 16 and the zero point of 8, where there are no zeros
+    // given) of a step's groups, one 16-row tile to a wave: read, add, put down
     const uint32_t unit = ZEROS ? 0xbf80bf80u : 0xc1c0c1c0u;
     const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{unit, unit, unit, unit});
-    auto add_x = [&](int s) {
-        const char *slot = lds + (s % C::RING) * C::STAGE;
-        for (int t = wave; t < C::BM / 16; t += C::WAVES)
+    const int sum_tile = wave % (C::BM / 16);
+    bf16x8 sx[4];
+    f32x4 sum_x[GP];
+    auto read_x = [&](int s) {
 #pragma unroll
-            for (int q = 0; q < GP; ++q) {
-                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 4; ++r) sx[r] = fragment(s, sum_tile, r);
+    };
+    auto add_x = [&]() {
 #pragma unroll
-                for (int r = q * PER; r < (q + 1) * PER; ++r) v = mfma16x16x32(fragment(slot, 16 * t + c16, r), minus, v);
-                if (c16 == 0) *reinterpret_cast<f32x4 *>(sums + (s & 1) * C::SUMS + q * C::BM + 16 * t + 4 * g) = v;
-            }
+        for (int q = 0; q < GP; ++q) {
+            sum_x[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int r = q * PER; r < (q + 1) * PER; ++r) sum_x[q] = mfma16x16x32(sx[r], minus, sum_x[q]);
+        }
+    };
+    auto put_sums = [&](int s) {
+        if (c16 == 0)
+#pragma unroll
+            for (int q = 0; q < GP; ++q)
+                *reinterpret_cast<f32x4 *>(sums + (s & 1) * C::SUMS + q * C::BM + 16 * sum_tile + 4 * g) = sum_x[q];
     };
 
+    const Widen widen;
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // Per step a wave issues NX copies, then its loads of codes (NW); waiting
-    // until that many are left therefore leaves the copies of two steps ahead
-    // in flight and has those of the next one done.
-    constexpr int NW = VEC ? NT : 4 * NT;
-    load_scales(0);
-    copy_x(0);
-    copy_x(1);
-    put_scales(0);
-    load_scales(1);
-    copy_x(2);
-    load_w(0);
-    wait_vm<2 * C::NX + NW>();
+    // Per step a wave issues NX + NW copies (and loads of scales); waiting
+    // until that many are left therefore has those issued two steps ago done
+    // and leaves the last step's in flight.
+    constexpr int COPIES = C::NX + C::NW * (VEC ? 1 : 4);
+    load_scales(0, 0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < C::NX; ++j) copy_x(s, j);
+    put_scales(0, 0);
+    load_scales(1, 1);
+    load_scales(2, 0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int j = 0; j < C::NW; ++j) copy_w(s, j);
+        if (s == 0)
+#pragma unroll
+            for (int j = 0; j < C::NX; ++j) copy_x(2, j);
+    }
+    wait_vm<COPIES>();
     __syncthreads();
-    add_x(0);
+    // X fragments of the step, each replaced by the next step's after its last use
+    bf16x8 xf[4][MT];
+    auto load_x = [&](int s, int r) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xf[r][i] = fragment(s, wm * MT + i, r);
+    };
+#pragma unroll
+    for (int r = 0; r < 4; ++r) load_x(0, r);
+    read_x(0);
+    add_x();
+    put_sums(0);
 
-    for (int s = 0; s < count; ++s) {
-        wait_vm<C::NX + NW>();
+    auto step = [&](int s, auto parity) {
+        constexpr int odd = decltype(parity)::value;
+        wait_vm<COPIES>();
         lds_wait_all();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        copy_x(s + 3);
-        u32x4 wc[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) wc[t] = arrange<GROUP>(w[t]);
-        load_w(s + 1);
-        put_scales(s + 1);
-        load_scales(s + 2);
-        add_x(s + 1);
-
-        const char *slot = lds + (s % C::RING) * C::STAGE;
         const float2 *scs = sc + (s & 1) * C::SCALES + wn * NT * 16 + c16;
         const float *xs = sums + (s & 1) * C::SUMS + wm * MT * 16 + 4 * g;
+        u32x4 w[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            w[t] = arrange<GROUP>(*reinterpret_cast<const u32x4 *>(wlds + (s % C::RING) * C::WSTAGE +
+                                                                   (wn * NT + t) * 1024 + c16 * 64 + g * 16));
 #pragma unroll
         for (int q = 0; q < GP; ++q) {
-            bf16x8 xf[MT][PER];
             f32x4 cs[MT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                cs[i] = *reinterpret_cast<const f32x4 *>(xs + q * C::BM + 16 * i);
-#pragma unroll
-                for (int r = 0; r < PER; ++r) xf[i][r] = fragment(slot, (wm * MT + i) * 16 + c16, q * PER + r);
-            }
+            for (int i = 0; i < MT; ++i) cs[i] = *reinterpret_cast<const f32x4 *>(xs + q * C::BM + 16 * i);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const float2 sz = scs[q * C::BN + 16 * t];
@@ -394,17 +472,47 @@ __global__ __launch_bounds__(WM *WN * 64) void quant_tile_kernel(QuantArgs a, in
 #pragma unroll
                 for (int i = 0; i < MT; ++i) p[i] = ZEROS ? cs[i] * sz.y : cs[i];
 #pragma unroll
-                for (int r = 0; r < PER; ++r) {
-                    const bf16x8 wf = widen(wc[t][q * PER + r]);
+                for (int r = q * PER; r < (q + 1) * PER; ++r) {
+                    const bf16x8 wf = widen(w[t][r]);
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) p[i] = mfma16x16x32(xf[i][r], wf, p[i]);
+                    for (int i = 0; i < MT; ++i) p[i] = mfma16x16x32(xf[r][i], wf, p[i]);
+                    if (t == NT - 1) load_x(s + 1, r);
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) acc[i][t][v] = __builtin_fmaf(sz.x, p[i][v], acc[i][t][v]);
+                // done here: moved to the step's end, the products of all its groups would be held at once
+#pragma unroll
+                for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[i][t]));
+
+                // What the coming steps need, a little after each tile: all
+                // waves are at the same place of a step, and issued together
+                // these stand in line for the memory pipeline while the matrix
+                // cores wait.
+                constexpr int H = GP * NT;
+                const int h = q * NT + t;
+                if (q == 0)
+#pragma unroll
+                    for (int j = t * C::NX / NT; j < (t + 1) * C::NX / NT; ++j) copy_x(s + 3, j);
+                if (q == 0)
+#pragma unroll
+                    for (int j = t * C::NW / NT; j < (t + 1) * C::NW / NT; ++j) copy_w(s + 2, j);
+                if (h == 0) read_x(s + 1);
+                if (h == 1) {
+                    add_x();
+                    put_scales(s + 1, odd ^ 1);
+                }
+                if (h == (H > 2 ? 2 : 1)) {
+                    load_scales(s + 3, odd ^ 1);
+                    put_sums(s + 1);
+                }
             }
         }
+    };
+    for (int s = 0; s < count; s += 2) {
+        step(s, std::integral_constant<int, 0>());
+        if (s + 1 < count) step(s + 1, std::integral_constant<int, 1>());
     }
     wait_vm<0>();
 
