@@ -19,6 +19,7 @@ struct QuantArgs {
     float *ws;              // split-K partials
     size_t ws_bytes;
     int cus;
+    int vec_scales = 0;     // set by the launcher: scales and zeros start at 16-byte boundaries
 };
 hipError_t launch_quant(const QuantArgs &a, hipStream_t st);
 

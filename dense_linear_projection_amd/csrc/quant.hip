@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
 // or the same quarter (groups of 32).  X is read in the same order.
 
 // An offset past every resource made here (they are below 2^31 bytes): a load there gives zero.
-constexpr uint32_t kOutside = 0xffffff00u;
+constexpr uint32_t kOutside = 0x80000000u;
 
 // Which of a step's sixteen words (and chunks of 8 x) lane group g holds in register r.
 template <int GROUP>
@@ -104,14 +104,10 @@ struct Widen {
     }
 };
 
-__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), 0, 0);
-}
-
 // Words 4 g .. 4 g + 3 of a step of one column; past the resource's end zero.
 // VEC: K is a multiple of 32, so that no load straddles that end.
 template <bool VEC>
-__device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step = 0) {
+__device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step) {
     if constexpr (VEC) {
         return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), static_cast<int>(step), 0);
     } else {
@@ -123,16 +119,20 @@ __device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t o
     }
 }
 
-// Up to 16 token rows: bound by reading the codes once, and at the smallest
-// sizes by the latency of doing so.  A workgroup owns 16 * NT columns; its
-// waves take steps in turn (two neighbouring ones at a time where there are
-// enough: 128 contiguous bytes of a column), straight from memory into
-// registers with DEPTH steps in flight and no barrier, and add up through LDS
-// at the end.  Nothing is split over workgroups, so there is one launch and no
-// workspace.  The columns' scales lie in LDS as fp32, staged `span` steps at
-// a time.
-template <int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
-__global__ __launch_bounds__(WAVES * 64) void quant_few_kernel(QuantArgs a, int span) {
+// Up to 64 token rows (16 MT): bound by reading the codes once, at the
+// smallest sizes by the latency of doing so.  A workgroup owns 16 NT columns;
+// its waves take steps in turn (two neighbouring ones at a time where there
+// are enough: 128 contiguous bytes of a column), codes and X straight from
+// memory into registers with no barrier, and add up through LDS at the end.
+// Nothing is split over workgroups, so there is one launch and no workspace.
+// A register is loaded for DEPTH steps ahead as soon as it has been used; with
+// more rows a step is long enough for the loads of the next one.  Words are
+// arranged as for groups of 32 whatever the group: then 16 rows of X are read
+// in runs of 64 bytes (in the other orders they are 16-byte pieces 64 apart,
+// four times the cache's cycles).  The columns' scales lie in LDS as fp32 and
+// their zero points as bytes, `span` steps at a time.
+template <int MT, int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
+__global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel(QuantArgs a, int span) {
     constexpr int GP = 128 / GROUP, PER = 4 / GP;  // groups of a step, registers of a group
     constexpr int COLS = 16 * NT, THREADS = WAVES * 64;
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -142,48 +142,103 @@ __global__ __launch_bounds__(WAVES * 64) void quant_few_kernel(QuantArgs a, int 
     const int cols = a.N - n0 < COLS ? static_cast<int>(a.N - n0) : COLS;
     const int M = static_cast<int>(a.M), steps = static_cast<int>((a.K + 127) / 128);
     const uint32_t words = static_cast<uint32_t>(a.K / 8);
-    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.codes + n0 * words, static_cast<uint32_t>(cols) * words * 4u);
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X, static_cast<uint32_t>(M) * words * 16u);
+    const uint32_t wbytes = static_cast<uint32_t>(cols) * words * 4u, xbytes = static_cast<uint32_t>(M) * words * 16u;
 
     const Widen widen;
-    f32x4 acc[NT];
+    f32x4 acc[MT][NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{0xbf80bf80u, 0xbf80bf80u, 0xbf80bf80u, 0xbf80bf80u});
+    // byte offsets of a lane's codes and X; columns and rows past the end lie outside the resources
+    uint32_t woff[NT], xoff[MT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) woff[t] = ((16u * t + c16) * words + 4u * g) * 4u;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xoff[i] = ((16u * i + c16) * words + g) * 16u;
 
     for (int from = 0; from < steps; from += span) {
         const int count = steps - from < span ? steps - from : span;
         const int pair = count >= 4 * WAVES ? 1 : 0;
         auto step_of = [&](int i) { return ((wave + WAVES * (i >> pair)) << pair) + (i & pair); };
-        u32x4 w[DEPTH][NT], x[DEPTH][4];
-        auto fetch = [&](int slot, int i) {
+        u32x4 w[DEPTH][NT], x[DEPTH][MT][4];
+        // steps past the end are read from empty resources: zeros
+        auto fetch_w = [&](int slot, int t, int i) {
             const int at = step_of(i);
-            const bool live = at < count;
+            const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.codes + n0 * words, at < count ? wbytes : 0u);
             const uint32_t word = static_cast<uint32_t>(from + at) * 16u;
+            const bool inside = word + 16 <= words;  // else the lanes' own offsets must show where the end is
+            w[slot][t] = load_words<VEC>(r, woff[t] + (inside ? 0u : word * 4u), inside ? word * 4u : 0u);
+        };
+        auto fetch_x = [&](int slot, int r, int i) {
+            const int at = step_of(i);
+            const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X, at < count ? xbytes : 0u);
+            const uint32_t word = static_cast<uint32_t>(from + at) * 16u;
+            // one code path: joining two would wait for their loads.  A chunk past the row is outside
+            const bool inside = word + 16 <= words;
+            const uint32_t by_lane = inside ? 0u : word * 16u, by_step = inside ? word * 16u : 0u;
+            const uint32_t past = word + 4u * r + g < words ? 0u : kOutside;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                w[slot][t] = load_words<VEC>(rw, live ? ((16u * t + c16) * words + word + 4u * g) * 4u : kOutside);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t k = word + word_of<GROUP>(r, g);
-                x[slot][r] = buffer_load16(rx, live && c16 < M && k < words ? (c16 * words + k) * 16u : kOutside);
-            }
+            for (int m = 0; m < MT; ++m)
+                x[slot][m][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, static_cast<int>(((xoff[m] + by_lane) | past) + 64u * r),
+                                                                      static_cast<int>(by_step), 0);
         };
 #pragma unroll
-        for (int i = 0; i < DEPTH; ++i) fetch(i, i);
+        for (int d = 0; d < DEPTH; ++d) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) fetch_w(d, t, d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) fetch_x(d, r, d);
+        }
 
-        // scales [column][group], rows an odd number of floats apart; behind them 16 + zero
-        const int groups = count * GP, row = groups | 1;
+        // scales [column][group], rows an odd number of words apart, and behind them the zero points
+        const int groups = count * GP, row = groups | 1, zrow = ((groups + 3) / 4 | 1) * 4;
         float *sc = reinterpret_cast<float *>(lds);
-        float *zc = sc + COLS * row;
+        uint8_t *zc = reinterpret_cast<uint8_t *>(sc + COLS * row);
         if (from > 0) __syncthreads();
-        for (int n = wave; n < COLS; n += WAVES)
-            for (int i = lane; i < groups; i += 64) {
-                const int64_t at = from * GP + i;
-                const bool ok = n < cols && at < a.G;
-                sc[n * row + i] = ok ? group_scale(a, (n0 + n) * a.G + at) : 0.f;
-                if (a.zeros) zc[n * row + i] = ok ? 16.f + static_cast<float>(a.zeros[(n0 + n) * a.G + at]) : 0.f;
-            }
+        const int64_t G = a.G, first = static_cast<int64_t>(from) * GP;
+        const int valid = G - first < groups ? static_cast<int>(G - first) : groups;
+        // a wave's lanes over `per` units of a row (a power of two) and 64 / per rows
+        auto over = [&](int units, auto &&f) {
+            const int shift = units >= 64 ? 6 : 32 - __builtin_clz(static_cast<unsigned>(units - 1 | 1));
+            const int rows = 64 >> shift;
+#pragma unroll 4
+            for (int n = wave * rows + (lane >> shift); n < COLS; n += WAVES * rows)
+                for (int i = lane & ((1 << shift) - 1); i < units; i += 1 << shift) f(n, i);
+        };
+        const int vec = a.scales_f32 ? 4 : 8;
+        if (G % 16 == 0 && first % 16 == 0 && valid % 16 == 0 && a.vec_scales) {
+            over(valid / vec, [&](int n, int i) {
+                u32x4 v = {0u, 0u, 0u, 0u};
+                const int64_t at = (n0 + n) * G + first + i * vec;
+                if (n < cols) v = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.scales) + at * (16 / vec));
+                float *to = sc + n * row + i * vec;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (a.scales_f32) {
+                        to[e] = __uint_as_float(v[e]);
+                    } else {
+                        to[2 * e] = __uint_as_float(v[e] << 16);
+                        to[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+                    }
+                }
+            });
+            if (a.zeros)
+                over(valid / 16, [&](int n, int i) {
+                    u32x4 v = {0u, 0u, 0u, 0u};
+                    if (n < cols) v = *reinterpret_cast<const u32x4 *>(a.zeros + (n0 + n) * G + first + i * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(zc + n * zrow + i * 16 + 4 * e) = v[e];
+                });
+        } else {
+            over(groups, [&](int n, int i) {
+                const bool ok = n < cols && i < valid;
+                const int64_t at = (n0 + n) * G + first + i;
+                sc[n * row + i] = ok ? group_scale(a, at) : 0.f;
+                if (a.zeros) zc[n * zrow + i] = ok ? a.zeros[at] : 0;
+            });
+        }
         __syncthreads();
 
         for (int i0 = 0; step_of(i0) < count; i0 += DEPTH) {
@@ -191,51 +246,68 @@ __global__ __launch_bounds__(WAVES * 64) void quant_few_kernel(QuantArgs a, int 
             for (int d = 0; d < DEPTH; ++d) {
                 const int at = step_of(i0 + d);
                 if (at >= count) break;
-                bf16x8 xv[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) xv[r] = __builtin_bit_cast(bf16x8, x[d][r]);
-                f32x4 minus_x[GP];
+                for (int t = 0; t < NT; ++t) w[d][t] = arrange<32>(w[d][t]);
 #pragma unroll
                 for (int q = 0; q < GP; ++q) {
-                    minus_x[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    f32x4 minus_x[MT];
 #pragma unroll
-                    for (int r = q * PER; r < (q + 1) * PER; ++r) minus_x[q] = mfma16x16x32(xv[r], minus, minus_x[q]);
-                }
+                    for (int m = 0; m < MT; ++m) {
+                        minus_x[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const u32x4 wt = arrange<GROUP>(w[d][t]);
+                        for (int r = q * PER; r < (q + 1) * PER; ++r)
+                            minus_x[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[d][m][r]), minus, minus_x[m]);
+                    }
 #pragma unroll
-                    for (int q = 0; q < GP; ++q) {
-                        const int si = (16 * t + c16) * row + at * GP + q;
-                        const float s = sc[si], z = a.zeros ? zc[si] : 24.f;
-                        f32x4 p = minus_x[q] * z;
+                    for (int t = 0; t < NT; ++t) {
+                        const int gi = at * GP + q;
+                        const float s = sc[(16 * t + c16) * row + gi];
+                        const float z = a.zeros ? 16.f + static_cast<float>(zc[(16 * t + c16) * zrow + gi]) : 24.f;
+                        f32x4 p[MT];
 #pragma unroll
-                        for (int r = q * PER; r < (q + 1) * PER; ++r) p = mfma16x16x32(xv[r], widen(wt[r]), p);
+                        for (int m = 0; m < MT; ++m) p[m] = minus_x[m] * z;
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[t][v] = __builtin_fmaf(s, p[v], acc[t][v]);
+                        for (int r = q * PER; r < (q + 1) * PER; ++r) {
+                            const bf16x8 wf = widen(w[d][t][r]);
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+                                p[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[d][m][r]), wf, p[m]);
+                            if (t == NT - 1) fetch_x(d, r, i0 + d + DEPTH);
+                        }
+                        if (q == GP - 1) fetch_w(d, t, i0 + d + DEPTH);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) acc[m][t][v] = __builtin_fmaf(s, p[m][v], acc[m][t][v]);
+                        // done here: moved to the step's end, the products of all its groups would be held at once
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(acc[m][t]));
                     }
                 }
-                fetch(d, i0 + d + DEPTH);
             }
         }
     }
 
-    // add the waves' sums; entry (row m, column n) at m * COLS + n
-    __syncthreads();
+    // add the waves' sums, 16 rows at a time
     float *red = reinterpret_cast<float *>(lds);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int i = 0; i < MT; ++i) {
+        __syncthreads();
 #pragma unroll
-        for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * g + v) * COLS + 16 * t + c16] = acc[t][v];
-    __syncthreads();
-    for (int e = tid; e < M * COLS; e += THREADS) {
-        const int m = e / COLS, n = e % COLS;
-        if (n >= cols) continue;
-        float y = 0.f;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) y += red[(i * 16 + m) * COLS + n];
-        const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n0 + n]) : 0.f;
-        store_out(a.Y, a.out, m * a.N + n0 + n, apply_epilogue(y, a.epi, b));
+            for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * g + v) * COLS + 16 * t + c16] = acc[i][t][v];
+        __syncthreads();
+        const int rows = M - 16 * i < 16 ? M - 16 * i : 16;
+        for (int e = tid; e < rows * COLS; e += THREADS) {
+            const int m = e / COLS, n = e % COLS;
+            if (n >= cols) continue;
+            float y = 0.f;
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) y += red[(k * 16 + m) * COLS + n];
+            const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n0 + n]) : 0.f;
+            store_out(a.Y, a.out, (16 * i + m) * a.N + n0 + n, apply_epilogue(y, a.epi, b));
+        }
     }
 }
 
@@ -587,17 +659,20 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
 }
 
 // Instantiated here: the launchers below are compiled for the host only.
-#define PROJ_QUANT_FEW(G, V)                                                                \
-    template __global__ void quant_few_kernel<1, 8, 4, G, V>(QuantArgs, int);               \
-    template __global__ void quant_few_kernel<2, 8, 3, G, V>(QuantArgs, int);               \
-    template __global__ void quant_few_kernel<4, 4, 3, G, V>(QuantArgs, int);
+#define PROJ_QUANT_WAVE(G, V)                                                               \
+    template __global__ void quant_wave_kernel<1, 1, 8, 4, G, V>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<1, 2, 8, 3, G, V>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<1, 4, 4, 3, G, V>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<2, 2, 8, 2, G, V>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<2, 4, 4, 2, G, V>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<4, 2, 8, 1, G, V>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<4, 4, 4, 1, G, V>(QuantArgs, int);
 #define PROJ_QUANT_TILE(G, Z, V)                                                            \
-    template __global__ void quant_tile_kernel<2, 2, 1, 4, G, Z, V>(QuantArgs, int);        \
     template __global__ void quant_tile_kernel<4, 2, 1, 4, G, Z, V>(QuantArgs, int);        \
     template __global__ void quant_tile_kernel<4, 4, 2, 4, G, Z, V>(QuantArgs, int);
-#define PROJ_QUANT_GROUP(G)      \
-    PROJ_QUANT_FEW(G, true)      \
-    PROJ_QUANT_FEW(G, false)     \
+#define PROJ_QUANT_GROUP(G)          \
+    PROJ_QUANT_WAVE(G, true)         \
+    PROJ_QUANT_WAVE(G, false)        \
     PROJ_QUANT_TILE(G, true, true)   \
     PROJ_QUANT_TILE(G, true, false)  \
     PROJ_QUANT_TILE(G, false, true)  \
@@ -614,29 +689,38 @@ static bool grid_for(int64_t items, int64_t per, unsigned *grid) {
     return true;
 }
 
-template <int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
-static hipError_t run_few(const QuantArgs &a, hipStream_t st) {
+template <int MT, int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
+static hipError_t run_wave(const QuantArgs &a, hipStream_t st) {
     unsigned grid;
     if (!grid_for(a.N, 16 * NT, &grid)) return hipErrorInvalidConfiguration;
-    constexpr int gp = 128 / GROUP, most = 64 << 10;
-    // as many steps' scales as 64 KB hold
+    constexpr int gp = 128 / GROUP, cols = 16 * NT;
+    // as many steps' scales as 64 KB hold: 4 and (with zeros) 1 byte a group, rows padded
     const int64_t steps = (a.K + 127) / 128;
-    const int per = a.zeros ? 8 : 4;
-    int64_t span = (most / (16 * NT * per) - 1) / gp;
+    int64_t span = (((64 << 10) / cols - 16) / (a.zeros ? 5 : 4) - 1) / gp;
+    if (span >= 16) span = span / 16 * 16;  // a later span starts at a multiple of 16 groups
     if (span > steps) span = steps;
-    const int64_t row = span * gp | 1;
-    int64_t lds = 16 * NT * row * per;
-    if (lds < WAVES * 1024 * NT) lds = WAVES * 1024 * NT;
-    hipLaunchKernelGGL((quant_few_kernel<NT, WAVES, DEPTH, GROUP, VEC>), dim3(grid), dim3(WAVES * 64),
+    const int64_t groups = span * gp;
+    int64_t lds = cols * ((groups | 1) * 4 + (a.zeros ? ((groups + 3) / 4 | 1) * 4 : 0));
+    if (lds < WAVES * 64 * cols) lds = WAVES * 64 * cols;
+    hipLaunchKernelGGL((quant_wave_kernel<MT, NT, WAVES, DEPTH, GROUP, VEC>), dim3(grid), dim3(WAVES * 64),
                        static_cast<unsigned>(lds), st, a, static_cast<int>(span));
     return hipGetLastError();
 }
 
 template <int GROUP, bool VEC>
-static hipError_t launch_few(const QuantArgs &a, hipStream_t st) {
-    if (a.N <= 16 * static_cast<int64_t>(a.cus)) return run_few<1, 8, 4, GROUP, VEC>(a, st);
-    if (a.N <= 64 * static_cast<int64_t>(a.cus)) return run_few<2, 8, 3, GROUP, VEC>(a, st);
-    return run_few<4, 4, 3, GROUP, VEC>(a, st);
+static hipError_t launch_wave(const QuantArgs &a, hipStream_t st) {
+    const int64_t cus = a.cus;
+    if (a.M <= 16) {
+        if (a.N <= 16 * cus) return run_wave<1, 1, 8, 4, GROUP, VEC>(a, st);
+        if (a.N <= 64 * cus) return run_wave<1, 2, 8, 3, GROUP, VEC>(a, st);
+        return run_wave<1, 4, 4, 3, GROUP, VEC>(a, st);
+    }
+    if (a.M <= 32) {
+        if (a.N <= 64 * cus) return run_wave<2, 2, 8, 2, GROUP, VEC>(a, st);
+        return run_wave<2, 4, 4, 2, GROUP, VEC>(a, st);
+    }
+    if (a.N <= 64 * cus) return run_wave<4, 2, 8, 1, GROUP, VEC>(a, st);
+    return run_wave<4, 4, 4, 1, GROUP, VEC>(a, st);
 }
 
 template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool VEC>
@@ -669,18 +753,19 @@ static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
 
 template <int GROUP, bool ZEROS, bool VEC>
 static hipError_t launch_tile(const QuantArgs &a, hipStream_t st) {
-    if (a.M <= 32) return run_tile<2, 2, 1, 4, GROUP, ZEROS, VEC>(a, st);
     if (((a.M + 127) / 128) * ((a.N + 255) / 256) * 2 > a.cus) return run_tile<4, 4, 2, 4, GROUP, ZEROS, VEC>(a, st);
     return run_tile<4, 2, 1, 4, GROUP, ZEROS, VEC>(a, st);
 }
 
 template <int GROUP, bool VEC>
 static hipError_t launch_group(const QuantArgs &a, hipStream_t st) {
-    if (a.M <= 16) return launch_few<GROUP, VEC>(a, st);
+    if (a.M <= 64) return launch_wave<GROUP, VEC>(a, st);
     return a.zeros ? launch_tile<GROUP, true, VEC>(a, st) : launch_tile<GROUP, false, VEC>(a, st);
 }
 
-hipError_t launch_quant(const QuantArgs &a, hipStream_t st) {
+hipError_t launch_quant(const QuantArgs &args, hipStream_t st) {
+    QuantArgs a = args;
+    a.vec_scales = (reinterpret_cast<uintptr_t>(a.scales) | reinterpret_cast<uintptr_t>(a.zeros)) % 16 == 0;
     // the matrix-core kernels read X in 16-byte chunks, and address a tile's
     // codes (at most 256 columns) and rows of X (128) with 32 bits
     if (a.K > 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.K < (int64_t{1} << 23)) {
