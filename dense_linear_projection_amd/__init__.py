@@ -27,7 +27,6 @@ cache between a decoding step's projections ``proj_kv_append`` and
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -160,10 +159,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # device index -> current stream's handle
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building torch's stream object costs 2.7 us, most of a small call's checks
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            _raw_stream = (lambda: get(dev())) if get and dev else lambda: torch.cuda.current_stream().cuda_stream
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -411,6 +418,34 @@ def _is_tensor(name, t, dtypes, shape=None):
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
 
 
+def _operand(name, t, dtypes, shape):
+    """Pointer of a contiguous device tensor of one of `dtypes` and of `shape` (a tuple); ValueError for another."""
+    if t.is_cuda and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _is_tensor(name, t, dtypes, shape)
+    raise ValueError("%s must be contiguous (row-major)" % name)
+
+
+class _Types:
+    """The operators' dtype tuples, made once torch is there."""
+
+    def __init__(self):
+        import torch
+        self.f32 = torch.float32
+        self.bf16, self.fp32, self.float = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
+        self.u8, self.i32, self.i64 = (torch.uint8,), (torch.int32,), (torch.int64,)
+
+
+_types = None
+
+
+def _dtypes():
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types
+
+
 def proj_pack_codes(ctx, q, codes=None, stream=None):
     """Lay out 4-bit codes given one to a byte (uint8 [N, K], K a multiple of
     8) as int32 words [N, K / 8] (allocated here if not given): of eight
@@ -454,10 +489,9 @@ def proj_run_quant(ctx, X, codes, scales, zeros, group, bias, epilogue, Y, strea
     8).  X bf16 [M, K], codes int32 [N, K / 8], scales bf16 or float32 and
     zeros uint8 [N, ceil(K / group)], bias bf16 [N] or None, Y float32 /
     bfloat16 [M, N]; all contiguous device tensors."""
-    import torch
-    bf16, f32 = torch.bfloat16, torch.float32
-    _is_tensor("X", X, (bf16,))
-    _is_tensor("codes", codes, (torch.int32,))
+    T = _types or _dtypes()
+    _is_tensor("X", X, T.bf16)
+    _is_tensor("codes", codes, T.i32)
     if X.dim() != 2 or codes.dim() != 2 or group not in (32, 64, 128):
         raise ValueError("X [M, K] and codes [N, K / 8] must have two dimensions, group 32, 64 or 128")
     M, K = X.shape
@@ -465,15 +499,14 @@ def proj_run_quant(ctx, X, codes, scales, zeros, group, bias, epilogue, Y, strea
     if words * 8 != K:
         raise ValueError("codes of %d words to a row do not fit K = %d" % (words, K))
     G = -(-K // group)
-    _is_tensor("scales", scales, (bf16, f32), (N, G))
-    if zeros is not None:
-        _is_tensor("zeros", zeros, (torch.uint8,), (N, G))
-    if bias is not None:
-        _is_tensor("bias", bias, (bf16,), (N,))
-    _is_tensor("Y", Y, (bf16, f32), (M, N))
-    _check(lib().proj_run_quant(ctx, _ptr(X), _ptr(codes), _ptr(scales), OUT_F32 if scales.dtype == f32 else OUT_BF16,
-                                _ptr(zeros), group, _ptr(bias), epilogue, M, N, K, _ptr(Y),
-                                OUT_F32 if Y.dtype == f32 else OUT_BF16, _stream(stream)), ctx)
+    f32 = T.f32
+    st = (_lib or lib()).proj_run_quant(
+        ctx, _ptr(X), _ptr(codes), _operand("scales", scales, T.float, (N, G)), OUT_F32 if scales.dtype == f32 else OUT_BF16,
+        None if zeros is None else _operand("zeros", zeros, T.u8, (N, G)), group,
+        None if bias is None else _operand("bias", bias, T.bf16, (N,)), epilogue, M, N, K,
+        _operand("Y", Y, T.float, (M, N)), OUT_F32 if Y.dtype == f32 else OUT_BF16, _stream(stream))
+    if st:
+        _check(st, ctx)
 
 
 # ------------------------------------------------- paged key-value cache
@@ -502,13 +535,13 @@ class kv_cache:
         self._p = ctypes.addressof(self._c)
 
 
-def _rows(name, t):
-    """Pointer and row stride (elements) of a tensor whose rows are contiguous."""
+def _rows(name, t, width):
+    """Pointer and row stride (elements) of a tensor whose rows, of `width` elements, are contiguous."""
     if t.is_contiguous():
-        return t.data_ptr(), t[0].numel() if t.shape[0] else math.prod(t.shape[1:])
+        return t.data_ptr(), width
     if not t[0].is_contiguous():
         raise ValueError("%s must have contiguous rows" % name)
-    return t.data_ptr(), t[0].numel() if t.shape[0] == 1 else t.stride(0)
+    return t.data_ptr(), width if t.shape[0] == 1 else t.stride(0)
 
 
 def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=None, interleaved=False,
@@ -519,8 +552,8 @@ def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=
     sines); queries go to q_out bf16 [T, q_heads, head_dim] (None: dropped),
     keys and values into the cache's slots (int64 [T], page * page_size +
     place; negative: a padding token, not stored)."""
-    import torch
-    _is_tensor("qkv", qkv, (torch.bfloat16,))
+    D = _types or _dtypes()
+    _is_tensor("qkv", qkv, D.bf16)
     if qkv.dim() != 2:
         raise ValueError("qkv must be [T, width]")
     T, width = qkv.shape
@@ -528,16 +561,16 @@ def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=
     if width % cache.head_dim or heads < 0 or (q_heads is not None and q_heads != heads):
         raise ValueError("qkv of width %d does not hold %s query and 2 * %d key-value heads of %d" %
                          (width, "any" if q_heads is None else q_heads, cache.heads, cache.head_dim))
-    _is_tensor("rope", rope, (torch.float32,))
+    _is_tensor("rope", rope, D.fp32)
     if rope.dim() != 2:
         raise ValueError("rope must be [positions, rot]")
-    _is_tensor("positions", positions, (torch.int32,), (T,))
-    _is_tensor("slots", slots, (torch.int64,), (T,))
-    if q_out is not None:
-        _is_tensor("q_out", q_out, (torch.bfloat16,), (T, heads, cache.head_dim))
-    x, stride = _rows("qkv", qkv)
-    _check(lib().proj_kv_append(ctx, cache._p, x, stride, T, heads, _ptr(rope), rope.shape[0], rope.shape[1],
-                                1 if interleaved else 0, _ptr(positions), _ptr(slots), _ptr(q_out), _stream(stream)), ctx)
+    x, stride = _rows("qkv", qkv, width)
+    st = (_lib or lib()).proj_kv_append(
+        ctx, cache._p, x, stride, T, heads, _ptr(rope), rope.shape[0], rope.shape[1], 1 if interleaved else 0,
+        _operand("positions", positions, D.i32, (T,)), _operand("slots", slots, D.i64, (T,)),
+        None if q_out is None else _operand("q_out", q_out, D.bf16, (T, heads, cache.head_dim)), _stream(stream))
+    if st:
+        _check(st, ctx)
 
 
 def proj_kv_attend(ctx, cache, q, tables, lengths, scale, out, lse=None, window=0, max_len=None, stream=None) -> None:
@@ -548,25 +581,24 @@ def proj_kv_attend(ctx, cache, q, tables, lengths, scale, out, lse=None, window=
     [B, q_heads, head_dim], lse float32 [B, q_heads] or None.  max_len bounds
     the lengths (default: what the tables hold); a tight one gives a better
     split."""
-    import torch
-    f32 = torch.float32
-    _is_tensor("q", q, (torch.bfloat16,))
+    T = _types or _dtypes()
+    _is_tensor("q", q, T.bf16)
     if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError("q must be [B, q_heads, %d]" % cache.head_dim)
-    B, heads, _ = q.shape
-    _is_tensor("tables", tables, (torch.int32,))
+    B, heads, D = q.shape
+    _is_tensor("tables", tables, T.i32)
     if tables.dim() != 2 or tables.shape[0] != B:
         raise ValueError("tables must be [B, width]")
-    _is_tensor("lengths", lengths, (torch.int32,), (B,))
-    _is_tensor("out", out, (torch.bfloat16, f32), q.shape)
-    if lse is not None:
-        _is_tensor("lse", lse, (f32,), (B, heads))
-    qp, stride = _rows("q", q)
-    tp, tstride = _rows("tables", tables)
     tw = tables.shape[1]
-    _check(lib().proj_kv_attend(ctx, cache._p, qp, stride, B, heads, tp, tstride, tw, _ptr(lengths),
-                                tw * cache.page_size if max_len is None else max_len, window, scale, _ptr(out),
-                                OUT_F32 if out.dtype == f32 else OUT_BF16, _ptr(lse), _stream(stream)), ctx)
+    qp, stride = _rows("q", q, heads * D)
+    tp, tstride = _rows("tables", tables, tw)
+    st = (_lib or lib()).proj_kv_attend(
+        ctx, cache._p, qp, stride, B, heads, tp, tstride, tw, _operand("lengths", lengths, T.i32, (B,)),
+        tw * cache.page_size if max_len is None else max_len, window, scale, _operand("out", out, T.float, (B, heads, D)),
+        OUT_F32 if out.dtype == T.f32 else OUT_BF16,
+        None if lse is None else _operand("lse", lse, T.fp32, (B, heads)), _stream(stream))
+    if st:
+        _check(st, ctx)
 
 
 def proj_graph_capture(ctx, Xs, Ws, biases, Ys, epilogue, out_dtype=None, stream=None) -> int:

@@ -43,6 +43,7 @@ typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
 
 constexpr int kChunk = 1024;       // tokens whose pages are staged at once
+constexpr int kJoined = 32;         // parts that the attention kernel joins itself
 constexpr float kLowest = -3e38f;  // a running maximum before the first logit
 
 // Four e4m3 bytes -> bf16, exact; two 32-bit words of pairs.
@@ -108,13 +109,27 @@ __device__ __forceinline__ void finish_head(const AttendArgs &a, int64_t at, int
         a.lse[row] = total == 0.f ? -__builtin_inff() : (most + log2f(total)) * 0.6931471805599453f;
 }
 
+// Two floats of a part's result: through the device's memory where another
+// workgroup of the same launch reads them.
+__device__ __forceinline__ void put_part(float *to, float x, float y, int shared) {
+    const uint64_t v = static_cast<uint64_t>(__float_as_uint(y)) << 32 | __float_as_uint(x);
+    if (shared)
+        __hip_atomic_store(reinterpret_cast<uint64_t *>(to), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else
+        *reinterpret_cast<uint64_t *>(to) = v;
+}
+__device__ __forceinline__ float2 get_part(const float *from) {
+    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t *>(from), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return float2{__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32))};
+}
+
 template <int D, bool FP8, int QT>
 __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
     using C = AttendCfg<D, FP8, QT>;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
     __shared__ uint32_t pages[kChunk + 2];
     __shared__ float top[4][16], sum[4][16];
-    __shared__ int wrong;
+    __shared__ int wrong, is_last;
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -348,12 +363,50 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
             const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + q0 + 16 * t + hq;
             if (parts > 1) {
                 float *to = a.ws + (row * a.parts + part) * (D + 4);
-                *reinterpret_cast<f32x4 *>(to + d) = v;
-                if (d == 0) *reinterpret_cast<float2 *>(to + D) = float2{most, total};
+                put_part(to + d, v[0], v[1], a.join);
+                put_part(to + d + 2, v[2], v[3], a.join);
+                if (d == 0) put_part(to + D, most, total, a.join);
             } else {
                 finish_head(a, row * D + d, row, d, v, most, total);
             }
         }
+    }
+    if (!a.join || parts <= 1) return;
+
+    // The last of the sequence's parts to finish joins them all: each
+    // workgroup counts itself once its stores have arrived, and the one that
+    // finds all others counted reads them.  The parts are stored and read past
+    // the dies' own caches, so waiting for the stores is all the order needed (a
+    // fence of device scope writes back a die's whole L2: with one in every
+    // workgroup 32 sequences of up to 16384 tokens took 724 us instead of 234).
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+        uint32_t *counter = a.counters + b * hh + hc;
+        is_last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
+                  static_cast<uint32_t>(parts);
+        if (is_last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!is_last) return;
+    const int heads = per - q0 < 16 * QT ? per - q0 : 16 * QT;
+    for (int e = tid; e < heads * (D / 4); e += 256) {
+        const int d = e % (D / 4) * 4;
+        const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + q0 + e / (D / 4);
+        const float *from = a.ws + row * a.parts * (D + 4);
+        float most = kLowest, total = 0.f;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) most = fmaxf(most, get_part(from + p * (D + 4) + D).x);
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) {
+            const float *x = from + p * (D + 4);
+            const float2 ml = get_part(x + D), lo = get_part(x + d), hi = get_part(x + d + 2);
+            const float f = exp2_hw(ml.x - most);
+            total += ml.y * f;
+            v += f32x4{lo.x, lo.y, hi.x, hi.y} * f;
+        }
+        finish_head(a, row * D + d, row, d, v, most, total);
     }
 }
 
@@ -445,6 +498,9 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     if (parts == 1) part = span > 0 ? span : 1;
     a.part = part;
     a.parts = static_cast<int>(parts);
+    // few parts are joined by the last workgroup; for many, one workgroup to
+    // each sequence's head is faster and the launch is hidden by the first kernel
+    a.join = parts > 1 && parts <= kJoined && rows <= a.ncounters;
     const int64_t grid = rows * parts;
     if (grid > 0x7fffffff || a.B * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
     auto kernel = a.c.fp8 ? attend_kernel<D, true, 1> : attend_kernel<D, false, 1>;
@@ -452,7 +508,7 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
         if (qt == 2) kernel = a.c.fp8 ? attend_kernel<D, true, 2> : attend_kernel<D, false, 2>;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || parts == 1) return e;
+    if (e != hipSuccess || parts == 1 || a.join) return e;
     hipLaunchKernelGGL((attend_join_kernel<D>), dim3(static_cast<unsigned>(a.B * a.q_heads)), dim3(256), 0, st, a);
     return hipGetLastError();
 }

@@ -14,6 +14,8 @@ struct ContextView {
     int cus;          // compute units of the device
     float *ws;        // the context's workspace, ws_bytes long
     size_t ws_bytes;
+    uint32_t *counters;  // ncounters of them, zero between calls: a kernel that counts sets its own back
+    int ncounters;
 };
 
 // PROJ_OK and the view of a live context, or the status of a call with `c`.

@@ -290,6 +290,8 @@ proj_status proj_kv_attend(proj_ctx *ctx, const proj_kv_cache *cache, const void
     a.ws = v.ws;
     a.ws_bytes = v.ws_bytes;
     a.cus = v.cus;
+    a.counters = v.counters;
+    a.ncounters = v.ncounters;
     return finish(ctx, launch_attend(a, static_cast<hipStream_t>(stream)));
 }
 

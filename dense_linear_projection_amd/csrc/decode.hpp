@@ -68,10 +68,13 @@ struct AttendArgs {
     float *ws;
     size_t ws_bytes;
     int cus;
+    uint32_t *counters = nullptr;  // zero between calls
+    int ncounters = 0;
     // set by the launcher: tokens of a part, parts of the longest sequence,
-    // chunks of a key-value head's query heads
+    // chunks of a key-value head's query heads, whether a sequence's last
+    // workgroup to finish joins its parts
     int64_t part = 0;
-    int parts = 0, chunks = 0;
+    int parts = 0, chunks = 0, join = 0;
 };
 hipError_t launch_attend(const AttendArgs &a, hipStream_t st);
 bool attend_dim(int dim);  // whether a kernel for this head size is built

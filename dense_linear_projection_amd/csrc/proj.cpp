@@ -49,6 +49,7 @@ constexpr uint32_t kMagic = 0x50524f4au;   // live context
 constexpr uint32_t kDead = 0xdeadbeefu;    // destroyed context
 constexpr size_t kZeroBytes = 256;   // zero page for masked loads
 constexpr size_t kSinkBytes = 1024;  // target of the read kernels' never-taken store
+constexpr int kCounters = 16384;     // counters of workgroups that have finished, zero between calls
 constexpr size_t kFlushBytes = 512ull << 20;  // larger than the last-level cache
 
 // K is the depth of the product: for a hi/lo weight pair (hilo = 1) twice
@@ -91,7 +92,7 @@ struct proj_ctx {
     double cu_flops;     // one CU's dense bf16 matrix rate (flop/s) at the device clock
     float *ws;           // split-K partial workspace, ws_bytes long (caller-bounded)
     size_t ws_bytes;
-    uint16_t *zeros;     // kZeroBytes of zeros, then kSinkBytes of sink (one allocation)
+    uint16_t *zeros;     // kZeroBytes of zeros, kSinkBytes of sink, then kCounters counters (one allocation)
     std::map<Key, Plan> plans;
     std::mutex mu;
     std::string err;
@@ -826,7 +827,8 @@ proj_status context_view(proj_ctx *c, ContextView *v) {
     if (!c) return PROJ_ERR_INVALID_ARG;
     if (c->magic == kDead) return PROJ_ERR_DESTROYED;
     if (c->magic != kMagic) return PROJ_ERR_INVALID_ARG;
-    *v = ContextView{c->device, c->cus, c->ws, c->ws_bytes};
+    uint32_t *counters = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(c->zeros) + kZeroBytes + kSinkBytes);
+    *v = ContextView{c->device, c->cus, c->ws, c->ws_bytes, counters, kCounters};
     return PROJ_OK;
 }
 
@@ -871,8 +873,8 @@ proj_status proj_create(proj_ctx **out, int device, size_t max_workspace_bytes) 
         delete c;
         return PROJ_ERR_HIP;
     }
-    bool ok = hipMalloc(&c->zeros, kZeroBytes + kSinkBytes) == hipSuccess &&
-              hipMemset(c->zeros, 0, kZeroBytes + kSinkBytes) == hipSuccess;
+    constexpr size_t fixed = kZeroBytes + kSinkBytes + kCounters * sizeof(uint32_t);
+    bool ok = hipMalloc(&c->zeros, fixed) == hipSuccess && hipMemset(c->zeros, 0, fixed) == hipSuccess;
     if (ok && max_workspace_bytes > 0) {
         const size_t ws = max_workspace_bytes / 256 * 256;
         if (ws > 0 && hipMalloc(&c->ws, ws) != hipSuccess) {
