@@ -13,10 +13,9 @@
 // A workgroup is four waves on one (sequence, key-value head, part); wave w
 // takes tiles w, w + 4, ... of 32 tokens, with its own running maximum, sum
 // and output, joined through LDS at the end, so the loop has no barrier.
-//   * w: v_mfma_f32_16x16x32_bf16 with A = 16 tokens of K, straight from
-//     global memory into registers (lane l: token l % 16, 8 elements), and
-//     B = 16 heads of q, held for the whole call.  A lane of the result has
-//     head l % 16 and tokens 4 (l / 16) + r.
+//   * w: v_mfma_f32_16x16x32_bf16 with A = 16 tokens of K (lane l: token
+//     l % 16, 8 elements) and B = 16 heads of q, held for the whole call.  A
+//     lane of the result has head l % 16 and tokens 4 (l / 16) + r.
 //   * o: A = V transposed (16 elements of the head x 32 tokens), B = the
 //     probabilities.  Two results of the first product, as they lie, are the
 //     32 tokens of B if slot 8 g + i of the product's k axis is token
@@ -28,11 +27,16 @@
 //     most is lost, below what the fp32 sum of a logit loses.  The
 //     second term is at least 1e-37 so that an infinite value does not meet
 //     a zero.
-//   * K and V of the next tile are loaded while this one is computed: 16 KB
-//     a wave in flight at 128 elements in bf16, and nothing waits for anything
-//     but its own operands.
+//   * K and V are read a KB at a time (whole rows, in the order they lie) into
+//     registers, put into LDS and read from there as the products need them;
+//     those of the next tile are on their way while this one is computed, 16 KB
+//     a wave at 128 elements in bf16, and nothing waits for anything but its own
+//     operands.  They are read once, and kept out of the caches
+//     (non-temporal loads, ONCE) unless heads share memory lines.
 // The running maximum moves only when a logit passes it by 2^8: sums stay in
 // range, and most tiles need no rescaling and no exchange between lanes.
+#include <type_traits>
+
 #include "decode.hpp"
 
 namespace proj {
@@ -42,7 +46,7 @@ typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
 typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
 
-constexpr int kChunk = 1024;       // tokens whose pages are staged at once
+constexpr int kChunk = 2048;       // tokens whose pages are staged at once
 constexpr int kJoined = 32;         // parts that the attention kernel joins itself
 constexpr float kLowest = -3e38f;  // a running maximum before the first logit
 
@@ -68,12 +72,14 @@ struct AttendCfg {
     static constexpr int KS = (D + 31) / 32;             // steps of the first product
     static constexpr int DT = D / 16;                    // tiles of the second
     static constexpr int VI = (32 * NC + 63) / 64;       // chunks of V to a lane
-    static constexpr int TILE = 32 * ROW;                // bytes of a tile of V in LDS
+    static constexpr int TILE = 32 * ROW;                // bytes of a tile of K or V in LDS
     static constexpr int ORED = 4 * 16 * (D + 4) * 4;    // the waves' outputs, 16 heads at a time
-    static constexpr int LDS = 4 * TILE > ORED ? 4 * TILE : ORED;
+    static constexpr int LDS = 8 * TILE > ORED ? 8 * TILE : ORED;
     // rows after which a row starts at the same LDS bank again
     static constexpr int PERIOD = ROW % 256 == 0 ? 1 : ROW % 128 == 0 ? 2 : ROW % 64 == 0 ? 4 : ROW % 32 == 0 ? 8 : 16;
-    // where chunk c of row r lies: turned by the row, so that the rows of one transposing load fall on different banks
+    // where chunk c of row r of K lies: turned by the row, so that one chunk of 16 rows falls on different banks
+    static __device__ __forceinline__ int place_k(int c, int r) { return (c + r / PERIOD) % NC; }
+    // the same for V and the rows of one transposing load
     static __device__ __forceinline__ int place(int c, int r) {
         const int turn = FP8 ? r / PERIOD + (r >= 16 ? 4 : 0) : 2 * (r / PERIOD);
         return (c + turn) % NC;
@@ -123,7 +129,7 @@ __device__ __forceinline__ float2 get_part(const float *from) {
     return float2{__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32))};
 }
 
-template <int D, bool FP8, int QT>
+template <int D, bool FP8, int QT, bool ONCE>
 __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
     using C = AttendCfg<D, FP8, QT>;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
@@ -134,8 +140,18 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int per = a.q_heads / a.c.heads;
-    // workgroup -> (sequence, part, head, chunk of the head's queries), heads fastest
-    const uint32_t hh = static_cast<uint32_t>(a.c.heads * a.chunks), u = blockIdx.x / hh, hc = blockIdx.x % hh;
+    // workgroup -> (sequence, part, head, chunk of the head's queries), heads
+    // fastest.  Ids go round the eight dies in turn: where the heads share
+    // memory lines, the heads of a part are given to one die (and the parts of a
+    // sequence to different ones), whose L2 then reads a line once.
+    const uint32_t hh = static_cast<uint32_t>(a.c.heads * a.chunks);
+    uint32_t u = blockIdx.x / hh, hc = blockIdx.x % hh;
+    if (a.by_die) {
+        const uint32_t die = blockIdx.x % 8, local = blockIdx.x / 8, group = local / hh;
+        hc = local % hh;
+        u = group * 8 + (die + group * 3) % 8;
+        if (u >= static_cast<uint32_t>(a.B * a.parts)) return;
+    }
     const int64_t b = u / static_cast<uint32_t>(a.parts);
     const int part = static_cast<int>(u % static_cast<uint32_t>(a.parts));
     const int h = static_cast<int>(hc) / a.chunks, q0 = static_cast<int>(hc) % a.chunks * (16 * QT);
@@ -169,8 +185,8 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
     const char *vb = static_cast<const char *>(a.c.v) + h * a.c.vh * (FP8 ? 1 : 2);
     const int64_t place_mask = (int64_t{1} << a.c.page_shift) - 1;
     const float to_exp2 = a.scale * a.c.k_scale * 1.4426950408889634f;
-    char *vt = lds + wave * C::TILE;
-    u32x4 kr[2][FP8 ? (C::KS + 1) / 2 : C::KS], vr[C::VI];
+    char *kt = lds + wave * 2 * C::TILE, *vt = kt + C::TILE;
+    u32x4 kr[C::VI], vr[C::VI];
 
     for (int64_t base = first; base < last; base += kChunk) {
         const int64_t end = last < base + kChunk ? last : base + kChunk;
@@ -195,45 +211,30 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                               static_cast<int64_t>(at & static_cast<int>(place_mask)) * token_stride;
             return FP8 ? e : 2 * e;
         };
-        auto load_k = [&](int j) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const char *p = kb + offset(32 * j + 16 * s + c16, a.c.kp, a.c.kt);
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int i = 0; i < D / 64; ++i) kr[s][i] = *reinterpret_cast<const u32x4 *>(p + 64 * i + 16 * g);
-                    if constexpr (D % 64 != 0) {
-                        u32x2 x = {0u, 0u};
-                        if (64 * (D / 64) + 8 * g < D) x = *reinterpret_cast<const u32x2 *>(p + 64 * (D / 64) + 8 * g);
-                        kr[s][D / 64] = u32x4{x[0], x[1], 0u, 0u};
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < C::KS; ++i) {
-                        if (32 * i + 32 <= D)
-                            kr[s][i] = *reinterpret_cast<const u32x4 *>(p + 64 * i + 16 * g);
-                        else
-                            kr[s][i] = 32 * i + 8 * g < D ? *reinterpret_cast<const u32x4 *>(p + 64 * i + 16 * g)
-                                                          : u32x4{0u, 0u, 0u, 0u};
-                    }
-                }
-            }
-        };
-        auto load_v = [&](int j) {
+        auto load = [&](u32x4 *r, const char *from, int j, int64_t page_stride, int64_t token_stride) {
 #pragma unroll
             for (int i = 0; i < C::VI; ++i) {
                 const int id = i * 64 + lane < 32 * C::NC ? i * 64 + lane : 32 * C::NC - 1;
-                const char *p = vb + offset(32 * j + id / C::NC, a.c.vp, a.c.vt);
-                vr[i] = *reinterpret_cast<const u32x4 *>(p + id % C::NC * 16);
+                const u32x4 *p = reinterpret_cast<const u32x4 *>(
+                    from + offset(32 * j + id / C::NC, page_stride, token_stride) + id % C::NC * 16);
+                r[i] = ONCE ? __builtin_nontemporal_load(p) : *p;
             }
         };
+        auto load_k = [&](int j) { load(kr, kb, j, a.c.kp, a.c.kt); };
+        auto load_v = [&](int j) { load(vr, vb, j, a.c.vp, a.c.vt); };
 
-        int j = wave;
-        if (j < tiles) {
-            load_k(j);
-            load_v(j);
+        // Workgroups start at different tiles: many run in step, and their
+        // tiles lie a power of two apart, which would gather their reads on
+        // few memory channels.
+        const int turn = static_cast<int>((static_cast<uint32_t>(part) * 5u + hc * 3u + static_cast<uint32_t>(b) * 7u) %
+                                          static_cast<uint32_t>(tiles));
+        auto tile_of = [&](int i) { return i >= tiles ? tiles : i + turn < tiles ? i + turn : i + turn - tiles; };
+        if (wave < tiles) {
+            load_k(tile_of(wave));
+            load_v(tile_of(wave));
         }
-        for (; j < tiles; j += 4) {
+        for (int i0 = wave; i0 < tiles; i0 += 4) {
+            const int j = tile_of(i0), next = tile_of(i0 + 4);
             const bool whole = 32 * j + 32 <= left;
             f32x4 s[QT][2];
 #pragma unroll
@@ -241,18 +242,32 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) s[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
+            for (int i = 0; i < C::VI; ++i) {
+                const int id = i * 64 + lane, r = id / C::NC;
+                if (64 * C::VI == 32 * C::NC || id < 32 * C::NC)
+                    *reinterpret_cast<u32x4 *>(kt + r * C::ROW + C::place_k(id % C::NC, r) * 16) = kr[i];
+            }
+            load_k(next);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
             for (int i = 0; i < C::KS; ++i)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    bf16x8 k;
-                    if constexpr (FP8)
-                        k = fp8x8_to_bf16(kr[x][i / 2][2 * (i % 2)], kr[x][i / 2][2 * (i % 2) + 1]);
-                    else
-                        k = __builtin_bit_cast(bf16x8, kr[x][i]);
+                    const int r = 16 * x + c16, e = C::element(i, g);
+                    bf16x8 k = bf16x8{};
+                    if (e < D) {
+                        const char *at = kt + r * C::ROW;
+                        if constexpr (FP8) {
+                            const u32x2 w = *reinterpret_cast<const u32x2 *>(at + C::place_k(e / 16, r) * 16 + e % 16);
+                            k = fp8x8_to_bf16(w[0], w[1]);
+                        } else {
+                            k = *reinterpret_cast<const bf16x8 *>(at + C::place_k(e / 8, r) * 16);
+                        }
+                    }
 #pragma unroll
                     for (int t = 0; t < QT; ++t) s[t][x] = mfma16x16x32(k, q[t][i], s[t][x]);
                 }
-            load_k(j + 4);
 
             bf16x8 hi[QT], lo[QT];
 #pragma unroll
@@ -295,7 +310,7 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                 if (64 * C::VI == 32 * C::NC || id < 32 * C::NC)
                     *reinterpret_cast<u32x4 *>(vt + r * C::ROW + C::place(id % C::NC, r) * 16) = vr[i];
             }
-            load_v(j + 4);
+            load_v(next);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -454,14 +469,17 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 }
 
 // Instantiated here: the launchers below are compiled for the host only.
-#define PROJ_ATTEND_INST(D)                                           \
-    template __global__ void attend_kernel<D, false, 1>(AttendArgs);  \
-    template __global__ void attend_kernel<D, true, 1>(AttendArgs);   \
+#define PROJ_ATTEND_QT(D, QT)                                               \
+    template __global__ void attend_kernel<D, false, QT, false>(AttendArgs); \
+    template __global__ void attend_kernel<D, false, QT, true>(AttendArgs);  \
+    template __global__ void attend_kernel<D, true, QT, false>(AttendArgs);  \
+    template __global__ void attend_kernel<D, true, QT, true>(AttendArgs);
+#define PROJ_ATTEND_INST(D) \
+    PROJ_ATTEND_QT(D, 1)    \
     template __global__ void attend_join_kernel<D>(AttendArgs);
-#define PROJ_ATTEND_INST2(D)                                          \
-    PROJ_ATTEND_INST(D)                                               \
-    template __global__ void attend_kernel<D, false, 2>(AttendArgs);  \
-    template __global__ void attend_kernel<D, true, 2>(AttendArgs);
+#define PROJ_ATTEND_INST2(D) \
+    PROJ_ATTEND_INST(D)      \
+    PROJ_ATTEND_QT(D, 2)
 PROJ_ATTEND_INST2(64)
 PROJ_ATTEND_INST2(80)
 PROJ_ATTEND_INST2(96)
@@ -483,11 +501,13 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     a.chunks = (per + 16 * qt - 1) / (16 * qt);
     const int64_t rows = a.B * a.c.heads * a.chunks;
     const int64_t span = a.window > 0 && a.window < a.max_len ? a.window : a.max_len;
-    // parts of the length: enough workgroups for four to a compute unit, none
-    // shorter than one tile for each wave nor longer than a staged chunk
-    // (lengths differ, and long parts would leave units idle at the end)
-    int64_t part = (span * rows + 4 * a.cus - 1) / (4 * a.cus);
-    part = part < 128 ? 128 : part > kChunk ? kChunk : (part + 127) / 128 * 128;
+    // Parts of the length: enough workgroups for four to a compute unit, none
+    // shorter than one tile for each wave, and none so long that units idle at
+    // the end where lengths differ.  One sequence has parts of one length: all
+    // of its workgroups (two to a unit) run at once.
+    const int64_t want = (a.B == 1 ? 2 : 4) * static_cast<int64_t>(a.cus), most = a.B == 1 ? kChunk : kChunk / 2;
+    int64_t part = (span * rows + want - 1) / want;
+    part = part < 128 ? 128 : part > most ? most : (part + 127) / 128 * 128;
     int64_t parts = span > part ? (span + part - 1) / part : 1;
     const int64_t room = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
     if (parts > 1 && parts > room) {
@@ -501,11 +521,23 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     // few parts are joined by the last workgroup; for many, one workgroup to
     // each sequence's head is faster and the launch is hidden by the first kernel
     a.join = parts > 1 && parts <= kJoined && rows <= a.ncounters;
-    const int64_t grid = rows * parts;
+    // Heads between a head's tokens (token-major pages): neighbouring heads'
+    // rows may share 128-byte lines
+    const int64_t size = a.c.fp8 ? 1 : 2;
+    const bool mixed = a.c.kt != D || a.c.vt != D;
+    const bool once = !mixed || (D * size % 128 == 0 && (a.c.kt | a.c.vt | a.c.kh | a.c.vh) * size % 128 == 0 &&
+                                 (reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v)) % 128 == 0);
+    a.by_die = mixed && a.B * parts >= 8;
+    const int64_t grid = a.by_die ? (a.B * parts + 7) / 8 * 8 * (a.c.heads * a.chunks) : rows * parts;
     if (grid > 0x7fffffff || a.B * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
-    auto kernel = a.c.fp8 ? attend_kernel<D, true, 1> : attend_kernel<D, false, 1>;
+    auto pick = [&](auto two) {
+        constexpr int QT = decltype(two)::value;
+        if (a.c.fp8) return once ? attend_kernel<D, true, QT, true> : attend_kernel<D, true, QT, false>;
+        return once ? attend_kernel<D, false, QT, true> : attend_kernel<D, false, QT, false>;
+    };
+    auto kernel = pick(std::integral_constant<int, 1>());
     if constexpr (kTwo)
-        if (qt == 2) kernel = a.c.fp8 ? attend_kernel<D, true, 2> : attend_kernel<D, false, 2>;
+        if (qt == 2) kernel = pick(std::integral_constant<int, 2>());
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1 || a.join) return e;

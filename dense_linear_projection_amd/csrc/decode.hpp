@@ -72,9 +72,9 @@ struct AttendArgs {
     int ncounters = 0;
     // set by the launcher: tokens of a part, parts of the longest sequence,
     // chunks of a key-value head's query heads, whether a sequence's last
-    // workgroup to finish joins its parts
+    // workgroup to finish joins its parts, whether a part's heads go to one die
     int64_t part = 0;
-    int parts = 0, chunks = 0, join = 0;
+    int parts = 0, chunks = 0, join = 0, by_die = 0;
 };
 hipError_t launch_attend(const AttendArgs &a, hipStream_t st);
 bool attend_dim(int dim);  // whether a kernel for this head size is built
