@@ -104,11 +104,15 @@ struct Widen {
     }
 };
 
+// How a row ends: kWhole at a step's end (K a multiple of 128), kPieces within
+// a step at the end of a lane's 16 bytes of codes (a multiple of 32), kWords
+// within those.
+enum Edge { kWhole = 0, kPieces = 1, kWords = 2 };
+
 // Words 4 g .. 4 g + 3 of a step of one column; past the resource's end zero.
-// VEC: K is a multiple of 32, so that no load straddles that end.
-template <bool VEC>
+template <int EDGE>
 __device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step) {
-    if constexpr (VEC) {
+    if constexpr (EDGE != kWords) {
         return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), static_cast<int>(step), 0);
     } else {
         u32x4 w;
@@ -125,13 +129,14 @@ __device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t o
 // are enough: 128 contiguous bytes of a column), codes and X straight from
 // memory into registers with no barrier, and add up through LDS at the end.
 // Nothing is split over workgroups, so there is one launch and no workspace.
-// A register is loaded for DEPTH steps ahead as soon as it has been used; with
-// more rows a step is long enough for the loads of the next one.  Words are
+// X is loaded DEPTH steps ahead, into registers that have just been used, and
+// codes WDEPTH: with 64 rows a step is long enough to hide the loads of the next
+// one's X.  Words are
 // arranged as for groups of 32 whatever the group: then 16 rows of X are read
 // in runs of 64 bytes (in the other orders they are 16-byte pieces 64 apart,
 // four times the cache's cycles).  The columns' scales lie in LDS as fp32 and
 // their zero points as bytes, `span` steps at a time.
-template <int MT, int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
+template <int MT, int NT, int WAVES, int DEPTH, int WDEPTH, int GROUP, int EDGE>
 __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel(QuantArgs a, int span) {
     constexpr int GP = 128 / GROUP, PER = 4 / GP;  // groups of a step, registers of a group
     constexpr int COLS = 16 * NT, THREADS = WAVES * 64;
@@ -162,34 +167,35 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
         const int count = steps - from < span ? steps - from : span;
         const int pair = count >= 4 * WAVES ? 1 : 0;
         auto step_of = [&](int i) { return ((wave + WAVES * (i >> pair)) << pair) + (i & pair); };
-        u32x4 w[DEPTH][NT], x[DEPTH][MT][4];
+        u32x4 w[WDEPTH][NT], x[DEPTH][MT][4];
         // steps past the end are read from empty resources: zeros
         auto fetch_w = [&](int slot, int t, int i) {
             const int at = step_of(i);
             const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.codes + n0 * words, at < count ? wbytes : 0u);
             const uint32_t word = static_cast<uint32_t>(from + at) * 16u;
-            const bool inside = word + 16 <= words;  // else the lanes' own offsets must show where the end is
-            w[slot][t] = load_words<VEC>(r, woff[t] + (inside ? 0u : word * 4u), inside ? word * 4u : 0u);
+            const bool inside = EDGE == kWhole || word + 16 <= words;  // else the lanes' offsets must show where the end is
+            w[slot][t] = load_words<EDGE>(r, woff[t] + (inside ? 0u : word * 4u), inside ? word * 4u : 0u);
         };
         auto fetch_x = [&](int slot, int r, int i) {
             const int at = step_of(i);
             const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X, at < count ? xbytes : 0u);
             const uint32_t word = static_cast<uint32_t>(from + at) * 16u;
             // one code path: joining two would wait for their loads.  A chunk past the row is outside
-            const bool inside = word + 16 <= words;
+            const bool inside = EDGE == kWhole || word + 16 <= words;
             const uint32_t by_lane = inside ? 0u : word * 16u, by_step = inside ? word * 16u : 0u;
-            const uint32_t past = word + 4u * r + g < words ? 0u : kOutside;
+            const uint32_t past = EDGE == kWhole || word + 4u * r + g < words ? 0u : kOutside;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
                 x[slot][m][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, static_cast<int>(((xoff[m] + by_lane) | past) + 64u * r),
                                                                       static_cast<int>(by_step), 0);
         };
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
+        for (int d = 0; d < WDEPTH; ++d) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) fetch_w(d, t, d);
+            if (d < DEPTH)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) fetch_x(d, r, d);
+                for (int r = 0; r < 4; ++r) fetch_x(d, r, d);
         }
 
         // scales [column][group], rows an odd number of words apart, and behind them the zero points
@@ -241,10 +247,12 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
         }
         __syncthreads();
 
-        for (int i0 = 0; step_of(i0) < count; i0 += DEPTH) {
+        for (int i0 = 0; step_of(i0) < count; i0 += WDEPTH) {
 #pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
+            for (int d = 0; d < WDEPTH; ++d) {
                 const int at = step_of(i0 + d);
+                constexpr int kRing = DEPTH;
+                const int dx = d % kRing;
                 if (at >= count) break;
 #pragma unroll
                 for (int t = 0; t < NT; ++t) w[d][t] = arrange<32>(w[d][t]);
@@ -256,7 +264,7 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
                         minus_x[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int r = q * PER; r < (q + 1) * PER; ++r)
-                            minus_x[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[d][m][r]), minus, minus_x[m]);
+                            minus_x[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[dx][m][r]), minus, minus_x[m]);
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
@@ -271,10 +279,9 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
                             const bf16x8 wf = widen(w[d][t][r]);
 #pragma unroll
                             for (int m = 0; m < MT; ++m)
-                                p[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[d][m][r]), wf, p[m]);
-                            if (t == NT - 1) fetch_x(d, r, i0 + d + DEPTH);
+                                p[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[dx][m][r]), wf, p[m]);
+                            if (t == NT - 1) fetch_x(dx, r, i0 + d + DEPTH);
                         }
-                        if (q == GP - 1) fetch_w(d, t, i0 + d + DEPTH);
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -284,6 +291,9 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
                         for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(acc[m][t]));
                     }
                 }
+                // behind X, whose next use comes first: loads complete in order
+#pragma unroll
+                for (int t = 0; t < NT; ++t) fetch_w(d, t, i0 + d + WDEPTH);
             }
         }
     }
@@ -337,7 +347,7 @@ struct TileCfg {
 // the scales and X of s + 3; one barrier a step publishes all of it.  Loads
 // complete in order, so whatever is used a step after its issue makes all that
 // was issued before it wait: everything is used two steps after.
-template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool VEC>
+template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, int EDGE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a, int splits) {
     using C = TileCfg<MT, NT, WM, WN, GROUP>;
     constexpr int GP = C::GP, PER = C::PER, THREADS = C::WAVES * 64;
@@ -393,7 +403,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         char *to = lds + (s % C::RING) * C::STAGE + (j * C::WAVES + wave) * 1024;
         const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.X + m0 * a.K, s < count ? xbytes : 0u);
         const uint32_t word = static_cast<uint32_t>(first + s) * 16u;
-        if (word + 16 <= words) {
+        if (EDGE == kWhole || word + 16 <= words) {
             dma16_buf(r, xoff[j], word * 16u, to);
         } else {
             const uint32_t row = static_cast<uint32_t>((j * C::WAVES + wave) * 4 + lane / 16);
@@ -406,8 +416,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         char *to = wlds + (s % C::RING) * C::WSTAGE + (j * C::WAVES + wave) * 1024;
         const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.codes + n0 * words, s < count ? wbytes : 0u);
         const uint32_t word = static_cast<uint32_t>(first + s) * 16u;
-        if constexpr (VEC) {
-            const bool inside = word + 16 <= words;
+        if constexpr (EDGE != kWords) {
+            const bool inside = EDGE == kWhole || word + 16 <= words;
             dma16_buf(r, woff[j] + (inside ? 0u : word * 4u), inside ? word * 4u : 0u, to);
         } else {
             // four bytes to a lane, so that none straddles the resource's end
@@ -427,7 +437,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
 #pragma unroll
         for (int i = 0; i < C::SI; ++i) {
             const uint32_t e = i * THREADS + tid;
-            const uint32_t off = GP == 1 || at + e % GP < G ? soff[i] + at : kOutside / 4;
+            const uint32_t off = EDGE == kWhole || GP == 1 || at + e % GP < G ? soff[i] + at : kOutside / 4;
             if (a.scales_f32)
                 sv[odd][i] = __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(off * 4u), 0, 0);
             else
@@ -488,7 +498,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
     // Per step a wave issues NX + NW copies (and loads of scales); waiting
     // until that many are left therefore has those issued two steps ago done
     // and leaves the last step's in flight.
-    constexpr int COPIES = C::NX + C::NW * (VEC ? 1 : 4);
+    constexpr int COPIES = C::NX + C::NW * (EDGE == kWords ? 4 : 1);
     load_scales(0, 0);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
@@ -659,24 +669,22 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
 }
 
 // Instantiated here: the launchers below are compiled for the host only.
-#define PROJ_QUANT_WAVE(G, V)                                                               \
-    template __global__ void quant_wave_kernel<1, 1, 8, 4, G, V>(QuantArgs, int);           \
-    template __global__ void quant_wave_kernel<1, 2, 8, 3, G, V>(QuantArgs, int);           \
-    template __global__ void quant_wave_kernel<1, 4, 4, 3, G, V>(QuantArgs, int);           \
-    template __global__ void quant_wave_kernel<2, 2, 8, 2, G, V>(QuantArgs, int);           \
-    template __global__ void quant_wave_kernel<2, 4, 4, 2, G, V>(QuantArgs, int);           \
-    template __global__ void quant_wave_kernel<4, 2, 8, 1, G, V>(QuantArgs, int);           \
-    template __global__ void quant_wave_kernel<4, 4, 4, 1, G, V>(QuantArgs, int);
-#define PROJ_QUANT_TILE(G, Z, V)                                                            \
-    template __global__ void quant_tile_kernel<4, 2, 1, 4, G, Z, V>(QuantArgs, int);        \
-    template __global__ void quant_tile_kernel<4, 4, 2, 4, G, Z, V>(QuantArgs, int);
-#define PROJ_QUANT_GROUP(G)          \
-    PROJ_QUANT_WAVE(G, true)         \
-    PROJ_QUANT_WAVE(G, false)        \
-    PROJ_QUANT_TILE(G, true, true)   \
-    PROJ_QUANT_TILE(G, true, false)  \
-    PROJ_QUANT_TILE(G, false, true)  \
-    PROJ_QUANT_TILE(G, false, false)
+#define PROJ_QUANT_EDGE(G, E)                                                               \
+    template __global__ void quant_wave_kernel<1, 1, 8, 4, 4, G, E>(QuantArgs, int);        \
+    template __global__ void quant_wave_kernel<1, 2, 8, 3, 3, G, E>(QuantArgs, int);        \
+    template __global__ void quant_wave_kernel<1, 4, 4, 3, 3, G, E>(QuantArgs, int);        \
+    template __global__ void quant_wave_kernel<2, 2, 8, 2, 2, G, E>(QuantArgs, int);        \
+    template __global__ void quant_wave_kernel<2, 4, 4, 2, 2, G, E>(QuantArgs, int);        \
+    template __global__ void quant_wave_kernel<4, 2, 8, 1, 2, G, E>(QuantArgs, int);        \
+    template __global__ void quant_wave_kernel<4, 4, 4, 1, 2, G, E>(QuantArgs, int);        \
+    template __global__ void quant_tile_kernel<4, 2, 1, 4, G, true, E>(QuantArgs, int);     \
+    template __global__ void quant_tile_kernel<4, 2, 1, 4, G, false, E>(QuantArgs, int);    \
+    template __global__ void quant_tile_kernel<4, 4, 2, 4, G, true, E>(QuantArgs, int);     \
+    template __global__ void quant_tile_kernel<4, 4, 2, 4, G, false, E>(QuantArgs, int);
+#define PROJ_QUANT_GROUP(G)    \
+    PROJ_QUANT_EDGE(G, kWhole)  \
+    PROJ_QUANT_EDGE(G, kPieces) \
+    PROJ_QUANT_EDGE(G, kWords)
 PROJ_QUANT_GROUP(32)
 PROJ_QUANT_GROUP(64)
 PROJ_QUANT_GROUP(128)
@@ -689,7 +697,7 @@ static bool grid_for(int64_t items, int64_t per, unsigned *grid) {
     return true;
 }
 
-template <int MT, int NT, int WAVES, int DEPTH, int GROUP, bool VEC>
+template <int MT, int NT, int WAVES, int DEPTH, int WDEPTH, int GROUP, int EDGE>
 static hipError_t run_wave(const QuantArgs &a, hipStream_t st) {
     unsigned grid;
     if (!grid_for(a.N, 16 * NT, &grid)) return hipErrorInvalidConfiguration;
@@ -702,28 +710,28 @@ static hipError_t run_wave(const QuantArgs &a, hipStream_t st) {
     const int64_t groups = span * gp;
     int64_t lds = cols * ((groups | 1) * 4 + (a.zeros ? ((groups + 3) / 4 | 1) * 4 : 0));
     if (lds < WAVES * 64 * cols) lds = WAVES * 64 * cols;
-    hipLaunchKernelGGL((quant_wave_kernel<MT, NT, WAVES, DEPTH, GROUP, VEC>), dim3(grid), dim3(WAVES * 64),
+    hipLaunchKernelGGL((quant_wave_kernel<MT, NT, WAVES, DEPTH, WDEPTH, GROUP, EDGE>), dim3(grid), dim3(WAVES * 64),
                        static_cast<unsigned>(lds), st, a, static_cast<int>(span));
     return hipGetLastError();
 }
 
-template <int GROUP, bool VEC>
+template <int GROUP, int EDGE>
 static hipError_t launch_wave(const QuantArgs &a, hipStream_t st) {
     const int64_t cus = a.cus;
     if (a.M <= 16) {
-        if (a.N <= 16 * cus) return run_wave<1, 1, 8, 4, GROUP, VEC>(a, st);
-        if (a.N <= 64 * cus) return run_wave<1, 2, 8, 3, GROUP, VEC>(a, st);
-        return run_wave<1, 4, 4, 3, GROUP, VEC>(a, st);
+        if (a.N <= 16 * cus) return run_wave<1, 1, 8, 4, 4, GROUP, EDGE>(a, st);
+        if (a.N <= 64 * cus) return run_wave<1, 2, 8, 3, 3, GROUP, EDGE>(a, st);
+        return run_wave<1, 4, 4, 3, 3, GROUP, EDGE>(a, st);
     }
     if (a.M <= 32) {
-        if (a.N <= 64 * cus) return run_wave<2, 2, 8, 2, GROUP, VEC>(a, st);
-        return run_wave<2, 4, 4, 2, GROUP, VEC>(a, st);
+        if (a.N <= 64 * cus) return run_wave<2, 2, 8, 2, 2, GROUP, EDGE>(a, st);
+        return run_wave<2, 4, 4, 2, 2, GROUP, EDGE>(a, st);
     }
-    if (a.N <= 64 * cus) return run_wave<4, 2, 8, 1, GROUP, VEC>(a, st);
-    return run_wave<4, 4, 4, 1, GROUP, VEC>(a, st);
+    if (a.N <= 64 * cus) return run_wave<4, 2, 8, 1, 2, GROUP, EDGE>(a, st);
+    return run_wave<4, 4, 4, 1, 2, GROUP, EDGE>(a, st);
 }
 
-template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool VEC>
+template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, int EDGE>
 static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
     using C = TileCfg<MT, NT, WM, WN, GROUP>;
     const int64_t tiles = ((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN), steps = (a.K + 127) / 128;
@@ -734,7 +742,7 @@ static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
     if (splits > room) splits = room;
     if (splits < 1) splits = 1;
     if (tiles * splits > 0x7fffffff) return hipErrorInvalidConfiguration;
-    auto kernel = quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, VEC>;
+    auto kernel = quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, EDGE>;
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                        C::LDS);
     if (e != hipSuccess) return e;
@@ -751,16 +759,22 @@ static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
     return launch_splitk_reduce(r, static_cast<int>(splits), st);
 }
 
-template <int GROUP, bool ZEROS, bool VEC>
+template <int GROUP, bool ZEROS, int EDGE>
 static hipError_t launch_tile(const QuantArgs &a, hipStream_t st) {
-    if (((a.M + 127) / 128) * ((a.N + 255) / 256) * 2 > a.cus) return run_tile<4, 4, 2, 4, GROUP, ZEROS, VEC>(a, st);
-    return run_tile<4, 2, 1, 4, GROUP, ZEROS, VEC>(a, st);
+    if (((a.M + 127) / 128) * ((a.N + 255) / 256) * 2 > a.cus) return run_tile<4, 4, 2, 4, GROUP, ZEROS, EDGE>(a, st);
+    return run_tile<4, 2, 1, 4, GROUP, ZEROS, EDGE>(a, st);
 }
 
-template <int GROUP, bool VEC>
+template <int GROUP, int EDGE>
 static hipError_t launch_group(const QuantArgs &a, hipStream_t st) {
-    if (a.M <= 64) return launch_wave<GROUP, VEC>(a, st);
-    return a.zeros ? launch_tile<GROUP, true, VEC>(a, st) : launch_tile<GROUP, false, VEC>(a, st);
+    if (a.M <= 64) return launch_wave<GROUP, EDGE>(a, st);
+    return a.zeros ? launch_tile<GROUP, true, EDGE>(a, st) : launch_tile<GROUP, false, EDGE>(a, st);
+}
+
+template <int GROUP>
+static hipError_t launch_edge(const QuantArgs &a, hipStream_t st) {
+    if (a.K % 128 == 0) return launch_group<GROUP, kWhole>(a, st);
+    return a.K % 32 == 0 ? launch_group<GROUP, kPieces>(a, st) : launch_group<GROUP, kWords>(a, st);
 }
 
 hipError_t launch_quant(const QuantArgs &args, hipStream_t st) {
@@ -769,11 +783,10 @@ hipError_t launch_quant(const QuantArgs &args, hipStream_t st) {
     // the matrix-core kernels read X in 16-byte chunks, and address a tile's
     // codes (at most 256 columns) and rows of X (128) with 32 bits
     if (a.K > 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 && a.K < (int64_t{1} << 23)) {
-        const bool vec = a.K % 32 == 0;
         switch (a.group) {
-            case 32: return vec ? launch_group<32, true>(a, st) : launch_group<32, false>(a, st);
-            case 64: return vec ? launch_group<64, true>(a, st) : launch_group<64, false>(a, st);
-            case 128: return vec ? launch_group<128, true>(a, st) : launch_group<128, false>(a, st);
+            case 32: return launch_edge<32>(a, st);
+            case 64: return launch_edge<64>(a, st);
+            case 128: return launch_edge<128>(a, st);
         }
     }
     unsigned grid;
