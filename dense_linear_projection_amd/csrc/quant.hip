@@ -127,21 +127,19 @@ __device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t o
     }
 }
 
-// Up to 64 token rows (16 MT): bound by reading the codes once, at the
+// Up to 32 token rows (16 MT): bound by reading the codes once, at the
 // smallest sizes by the latency of doing so.  A workgroup owns 16 NT columns;
 // its waves take steps in turn (two neighbouring ones at a time where there
-// are enough: 128 contiguous bytes of a column), codes and X straight from
-// memory into registers with no barrier, and add up through LDS at the end.
-// Nothing is split over workgroups, so there is one launch and no workspace.
-// X is loaded DEPTH steps ahead, into registers that have just been used, and
-// codes WDEPTH: with 64 rows a step is long enough to hide the loads of the next
-// one's X.  Words are
-// arranged as for groups of 32 whatever the group: then 16 rows of X are read
-// in runs of 64 bytes (in the other orders they are 16-byte pieces 64 apart,
-// four times the cache's cycles).  The columns' scales lie in LDS as fp32 and
-// their zero points as bytes, `span` steps at a time.
-template <int MT, int NT, int WAVES, int DEPTH, int WDEPTH, int GROUP, int EDGE>
-__global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel(QuantArgs a, int span) {
+// are enough: 128 contiguous bytes of a column) with no barrier, and add up
+// through LDS at the end.  Nothing is split over workgroups, so there is one
+// launch and no workspace.  Neighbouring lanes read neighbouring 16 bytes
+// (the cache takes a load whose lanes do not lie in runs one lane at a time:
+// 64 cycles instead of 16), DEPTH steps ahead, into registers, and pass them on
+// to the lanes that need them through a piece of LDS of the wave's own.  The
+// columns' scales lie in LDS as fp32 and their zero points (8 where none are
+// given) as bytes, `span` steps at a time.
+template <int MT, int NT, int WAVES, int DEPTH, int GROUP, int EDGE>
+__global__ __launch_bounds__(WAVES * 64) void quant_wave_kernel(QuantArgs a, int span) {
     constexpr int GP = 128 / GROUP, PER = 4 / GP;  // groups of a step, registers of a group
     constexpr int COLS = 16 * NT, THREADS = WAVES * 64;
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -160,51 +158,47 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{0xbf80bf80u, 0xbf80bf80u, 0xbf80bf80u, 0xbf80bf80u});
-    // byte offsets of a lane's codes and X; columns and rows past the end lie outside the resources
-    uint32_t woff[NT], xoff[MT];
+    // byte offsets of a lane's codes (column lane / 4, piece lane % 4) and X (row
+    // lane / 16 of four, chunk lane % 16); columns and rows past the end lie
+    // outside the resources
+    constexpr int XI = 4 * MT;  // loads of X a step
+    uint32_t woff[NT], xoff[XI];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) woff[t] = ((16u * t + c16) * words + 4u * g) * 4u;
+    for (int t = 0; t < NT; ++t) woff[t] = ((16u * t + lane / 4) * words + 4u * (lane % 4)) * 4u;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) xoff[i] = ((16u * i + c16) * words + g) * 16u;
+    for (int i = 0; i < XI; ++i) xoff[i] = ((4u * i + lane / 16) * words + c16) * 16u;
+    // the wave's own LDS: its codes, then X with chunk c of row m at c ^ m % 16
+    char *own = lds + wave * (NT * 1024 + MT * 4096);
+    char *scales = lds + WAVES * (NT * 1024 + MT * 4096);
 
     for (int from = 0; from < steps; from += span) {
         const int count = steps - from < span ? steps - from : span;
         const int pair = count >= 4 * WAVES ? 1 : 0;
         auto step_of = [&](int i) { return ((wave + WAVES * (i >> pair)) << pair) + (i & pair); };
-        u32x4 w[WDEPTH][NT], x[DEPTH][MT][4];
+        u32x4 w[DEPTH][NT], x[DEPTH][XI];
         // steps past the end are read from empty resources: zeros
-        auto fetch_w = [&](int slot, int t, int i) {
+        auto fetch = [&](int slot, int i) {
             const int at = step_of(i);
-            const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.codes + n0 * words, at < count ? wbytes : 0u);
-            const uint32_t word = static_cast<uint32_t>(from + at) * 16u;
-            const bool inside = EDGE == kWhole || word + 16 <= words;  // else the lanes' offsets must show where the end is
-            w[slot][t] = load_words<EDGE>(r, woff[t] + (inside ? 0u : word * 4u), inside ? word * 4u : 0u);
-        };
-        auto fetch_x = [&](int slot, int r, int i) {
-            const int at = step_of(i);
+            const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.codes + n0 * words, at < count ? wbytes : 0u);
             const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X, at < count ? xbytes : 0u);
             const uint32_t word = static_cast<uint32_t>(from + at) * 16u;
-            // one code path: joining two would wait for their loads.  A chunk past the row is outside
+            // in a row's last step, if it is short, the lanes' own offsets must show where the end is
             const bool inside = EDGE == kWhole || word + 16 <= words;
-            const uint32_t by_lane = inside ? 0u : word * 16u, by_step = inside ? word * 16u : 0u;
-            const uint32_t past = EDGE == kWhole || word + 4u * r + g < words ? 0u : kOutside;
+            const uint32_t by_lane = inside ? 0u : word, by_step = inside ? word : 0u;
+            const uint32_t past = EDGE == kWhole || word + c16 < words ? 0u : kOutside;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-                x[slot][m][r] = __builtin_amdgcn_raw_buffer_load_b128(rx, static_cast<int>(((xoff[m] + by_lane) | past) + 64u * r),
-                                                                      static_cast<int>(by_step), 0);
+            for (int t = 0; t < NT; ++t) w[slot][t] = load_words<EDGE>(rw, woff[t] + by_lane * 4u, by_step * 4u);
+#pragma unroll
+            for (int j = 0; j < XI; ++j)
+                x[slot][j] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rx, static_cast<int>((xoff[j] + by_lane * 16u) | past), static_cast<int>(by_step * 16u), 0);
         };
 #pragma unroll
-        for (int d = 0; d < WDEPTH; ++d) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) fetch_w(d, t, d);
-            if (d < DEPTH)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) fetch_x(d, r, d);
-        }
+        for (int d = 0; d < DEPTH; ++d) fetch(d, d);
 
         // scales [column][group], rows an odd number of words apart, and behind them the zero points
         const int groups = count * GP, row = groups | 1, zrow = ((groups + 3) / 4 | 1) * 4;
-        float *sc = reinterpret_cast<float *>(lds);
+        float *sc = reinterpret_cast<float *>(scales);
         uint8_t *zc = reinterpret_cast<uint8_t *>(sc + COLS * row);
         if (from > 0) __syncthreads();
         const int64_t G = a.G, first = static_cast<int64_t>(from) * GP;
@@ -234,32 +228,48 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
                     }
                 }
             });
-            if (a.zeros)
-                over(valid / 16, [&](int n, int i) {
-                    u32x4 v = {0u, 0u, 0u, 0u};
-                    if (n < cols) v = *reinterpret_cast<const u32x4 *>(a.zeros + (n0 + n) * G + first + i * 16);
+            over(valid / 16, [&](int n, int i) {
+                u32x4 v = {0x08080808u, 0x08080808u, 0x08080808u, 0x08080808u};
+                if (n < cols && a.zeros) v = *reinterpret_cast<const u32x4 *>(a.zeros + (n0 + n) * G + first + i * 16);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(zc + n * zrow + i * 16 + 4 * e) = v[e];
-                });
+                for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(zc + n * zrow + i * 16 + 4 * e) = v[e];
+            });
         } else {
             over(groups, [&](int n, int i) {
                 const bool ok = n < cols && i < valid;
                 const int64_t at = (n0 + n) * G + first + i;
                 sc[n * row + i] = ok ? group_scale(a, at) : 0.f;
-                if (a.zeros) zc[n * zrow + i] = ok ? a.zeros[at] : 0;
+                zc[n * zrow + i] = ok && a.zeros ? a.zeros[at] : 8;
             });
         }
         __syncthreads();
 
-        for (int i0 = 0; step_of(i0) < count; i0 += WDEPTH) {
+        for (int i0 = 0; step_of(i0) < count; i0 += DEPTH) {
 #pragma unroll
-            for (int d = 0; d < WDEPTH; ++d) {
+            for (int d = 0; d < DEPTH; ++d) {
                 const int at = step_of(i0 + d);
-                constexpr int kRing = DEPTH;
-                const int dx = d % kRing;
                 if (at >= count) break;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) w[d][t] = arrange<32>(w[d][t]);
+                for (int t = 0; t < NT; ++t) *reinterpret_cast<u32x4 *>(own + t * 1024 + lane * 16) = w[d][t];
+#pragma unroll
+                for (int j = 0; j < XI; ++j) {
+                    const int r = 4 * j + lane / 16;
+                    *reinterpret_cast<u32x4 *>(own + NT * 1024 + r * 256 + ((c16 ^ (r & 15)) << 4)) = x[d][j];
+                }
+                fetch(d, i0 + d + DEPTH);
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+                bf16x8 xv[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        xv[m][r] = *reinterpret_cast<const bf16x8 *>(own + NT * 1024 + (16 * m + c16) * 256 +
+                                                                     ((word_of<GROUP>(r, g) ^ c16) << 4));
+                u32x4 wv[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    wv[t] = arrange<GROUP>(*reinterpret_cast<const u32x4 *>(own + t * 1024 + c16 * 64 + g * 16));
 #pragma unroll
                 for (int q = 0; q < GP; ++q) {
                     f32x4 minus_x[MT];
@@ -267,24 +277,23 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
                     for (int m = 0; m < MT; ++m) {
                         minus_x[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int r = q * PER; r < (q + 1) * PER; ++r)
-                            minus_x[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[dx][m][r]), minus, minus_x[m]);
+                        for (int r = q * PER; r < (q + 1) * PER; ++r) minus_x[m] = mfma16x16x32(xv[m][r], minus, minus_x[m]);
                     }
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const int gi = at * GP + q;
                         const float s = sc[(16 * t + c16) * row + gi];
-                        const float z = a.zeros ? 16.f + static_cast<float>(zc[(16 * t + c16) * zrow + gi]) : 24.f;
+                        // no branch on a.zeros here: the compiler leaves too few wait states between a
+                        // matrix product and its result's use behind the join of two branches
+                        const float z = 16.f + static_cast<float>(zc[(16 * t + c16) * zrow + gi]);
                         f32x4 p[MT];
 #pragma unroll
                         for (int m = 0; m < MT; ++m) p[m] = minus_x[m] * z;
 #pragma unroll
                         for (int r = q * PER; r < (q + 1) * PER; ++r) {
-                            const bf16x8 wf = widen(w[d][t][r]);
+                            const bf16x8 wf = widen(wv[t][r]);
 #pragma unroll
-                            for (int m = 0; m < MT; ++m)
-                                p[m] = mfma16x16x32(__builtin_bit_cast(bf16x8, x[dx][m][r]), wf, p[m]);
-                            if (t == NT - 1) fetch_x(dx, r, i0 + d + DEPTH);
+                            for (int m = 0; m < MT; ++m) p[m] = mfma16x16x32(xv[m][r], wf, p[m]);
                         }
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
@@ -295,14 +304,13 @@ __global__ __launch_bounds__(WAVES * 64, MT == 4 ? 2 : 1) void quant_wave_kernel
                         for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(acc[m][t]));
                     }
                 }
-                // behind X, whose next use comes first: loads complete in order
-#pragma unroll
-                for (int t = 0; t < NT; ++t) fetch_w(d, t, i0 + d + WDEPTH);
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
             }
         }
     }
 
-    // add the waves' sums, 16 rows at a time
+    // add the waves' sums, 16 rows at a time, over their pieces of LDS (1 KB for each tile of columns)
     float *red = reinterpret_cast<float *>(lds);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -674,13 +682,11 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
 
 // Instantiated here: the launchers below are compiled for the host only.
 #define PROJ_QUANT_EDGE(G, E)                                                               \
-    template __global__ void quant_wave_kernel<1, 1, 8, 4, 4, G, E>(QuantArgs, int);        \
-    template __global__ void quant_wave_kernel<1, 2, 8, 3, 3, G, E>(QuantArgs, int);        \
-    template __global__ void quant_wave_kernel<1, 4, 4, 3, 3, G, E>(QuantArgs, int);        \
-    template __global__ void quant_wave_kernel<2, 2, 8, 2, 2, G, E>(QuantArgs, int);        \
-    template __global__ void quant_wave_kernel<2, 4, 4, 2, 2, G, E>(QuantArgs, int);        \
-    template __global__ void quant_wave_kernel<4, 2, 8, 1, 2, G, E>(QuantArgs, int);        \
-    template __global__ void quant_wave_kernel<4, 4, 4, 1, 2, G, E>(QuantArgs, int);        \
+    template __global__ void quant_wave_kernel<1, 1, 8, 4, G, E>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<1, 2, 8, 3, G, E>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<1, 4, 4, 3, G, E>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<2, 2, 8, 2, G, E>(QuantArgs, int);           \
+    template __global__ void quant_wave_kernel<2, 4, 4, 2, G, E>(QuantArgs, int);           \
     template __global__ void quant_tile_kernel<4, 2, 1, 4, G, true, E>(QuantArgs, int);     \
     template __global__ void quant_tile_kernel<4, 2, 1, 4, G, false, E>(QuantArgs, int);    \
     template __global__ void quant_tile_kernel<4, 4, 2, 4, G, true, E>(QuantArgs, int);     \
@@ -701,21 +707,27 @@ static bool grid_for(int64_t items, int64_t per, unsigned *grid) {
     return true;
 }
 
-template <int MT, int NT, int WAVES, int DEPTH, int WDEPTH, int GROUP, int EDGE>
+template <int MT, int NT, int WAVES, int DEPTH, int GROUP, int EDGE>
 static hipError_t run_wave(const QuantArgs &a, hipStream_t st) {
     unsigned grid;
     if (!grid_for(a.N, 16 * NT, &grid)) return hipErrorInvalidConfiguration;
     constexpr int gp = 128 / GROUP, cols = 16 * NT;
-    // as many steps' scales as 64 KB hold: 4 and (with zeros) 1 byte a group, rows padded
+    // the waves' own pieces, and the scales of as many steps as fit into 44 KB
+    // beside them: 5 bytes a group, rows padded
+    constexpr int pieces = WAVES * (NT * 1024 + MT * 4096);
     const int64_t steps = (a.K + 127) / 128;
-    int64_t span = (((64 << 10) / cols - 16) / (a.zeros ? 5 : 4) - 1) / gp;
+    int64_t span = (((44 << 10) / cols - 16) / 5 - 1) / gp;
     if (span >= 16) span = span / 16 * 16;  // a later span starts at a multiple of 16 groups
     if (span > steps) span = steps;
     const int64_t groups = span * gp;
-    int64_t lds = cols * ((groups | 1) * 4 + (a.zeros ? ((groups + 3) / 4 | 1) * 4 : 0));
-    if (lds < WAVES * 64 * cols) lds = WAVES * 64 * cols;
-    hipLaunchKernelGGL((quant_wave_kernel<MT, NT, WAVES, DEPTH, WDEPTH, GROUP, EDGE>), dim3(grid), dim3(WAVES * 64),
-                       static_cast<unsigned>(lds), st, a, static_cast<int>(span));
+    int64_t lds = pieces + cols * ((groups | 1) * 4 + ((groups + 3) / 4 | 1) * 4);
+    auto kernel = quant_wave_kernel<MT, NT, WAVES, DEPTH, GROUP, EDGE>;
+    if (lds > (64 << 10)) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(WAVES * 64), static_cast<unsigned>(lds), st, a, static_cast<int>(span));
     return hipGetLastError();
 }
 
@@ -723,16 +735,12 @@ template <int GROUP, int EDGE>
 static hipError_t launch_wave(const QuantArgs &a, hipStream_t st) {
     const int64_t cus = a.cus;
     if (a.M <= 16) {
-        if (a.N <= 16 * cus) return run_wave<1, 1, 8, 4, 4, GROUP, EDGE>(a, st);
-        if (a.N <= 64 * cus) return run_wave<1, 2, 8, 3, 3, GROUP, EDGE>(a, st);
-        return run_wave<1, 4, 4, 3, 3, GROUP, EDGE>(a, st);
+        if (a.N <= 16 * cus) return run_wave<1, 1, 8, 4, GROUP, EDGE>(a, st);
+        if (a.N <= 64 * cus) return run_wave<1, 2, 8, 3, GROUP, EDGE>(a, st);
+        return run_wave<1, 4, 4, 3, GROUP, EDGE>(a, st);
     }
-    if (a.M <= 32) {
-        if (a.N <= 64 * cus) return run_wave<2, 2, 8, 2, 2, GROUP, EDGE>(a, st);
-        return run_wave<2, 4, 4, 2, 2, GROUP, EDGE>(a, st);
-    }
-    if (a.N <= 64 * cus) return run_wave<4, 2, 8, 1, 2, GROUP, EDGE>(a, st);
-    return run_wave<4, 4, 4, 1, 2, GROUP, EDGE>(a, st);
+    if (a.N <= 64 * cus) return run_wave<2, 2, 8, 2, GROUP, EDGE>(a, st);
+    return run_wave<2, 4, 4, 2, GROUP, EDGE>(a, st);
 }
 
 template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, int EDGE>
@@ -771,7 +779,7 @@ static hipError_t launch_tile(const QuantArgs &a, hipStream_t st) {
 
 template <int GROUP, int EDGE>
 static hipError_t launch_group(const QuantArgs &a, hipStream_t st) {
-    if (a.M <= 64) return launch_wave<GROUP, EDGE>(a, st);
+    if (a.M <= 32) return launch_wave<GROUP, EDGE>(a, st);
     return a.zeros ? launch_tile<GROUP, true, EDGE>(a, st) : launch_tile<GROUP, false, EDGE>(a, st);
 }
 
