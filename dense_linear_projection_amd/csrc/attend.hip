@@ -22,11 +22,12 @@
 //     4 g + i (i < 4) or 16 + 4 g + i - 4; V follows by being read in that
 //     order with LDS's transposing loads.  So the probabilities never leave
 //     the registers.
-//   * a probability enters as two bf16 terms, its upper 8 bits (cut, so that
-//     the rest is never negative) and the rest rounded: 2^-16 of its value at
-//     most is lost, below what the fp32 sum of a logit loses.  The
-//     second term is at least 1e-37 so that an infinite value does not meet
-//     a zero.
+//   * a probability enters as bf16 terms of 8 bits each: for fp32 results three,
+//     which together are its 24 bits; for bf16 results two (48 sequences with a
+//     window: 17.3 us with two, 21.9 with three; two leave fp32 results 4e-6 off
+//     where three leave 3e-7).  They are cut, not rounded, so that what is left
+//     is never negative, and those after the first are at least 1e-37, so that an
+//     infinite value does not meet a zero.
 //   * K and V are read a KB at a time (whole rows, in the order they lie) into
 //     registers, put into LDS and read from there as the products need them;
 //     those of the next tile are on their way while this one is computed, 16 KB
@@ -44,7 +45,6 @@ namespace proj {
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
 typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
-typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
 
 constexpr int kChunk = 2048;       // tokens whose pages are staged at once
 constexpr int kJoined = 32;         // parts that the attention kernel joins itself
@@ -129,8 +129,9 @@ __device__ __forceinline__ float2 get_part(const float *from) {
     return float2{__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32))};
 }
 
-template <int D, bool FP8, int QT, bool ONCE>
-__global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
+// Two workgroups to a compute unit where their registers (and 160 KB of LDS) allow it.
+template <int D, bool FP8, int QT, bool ONCE, int TERMS>
+__global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(AttendArgs a) {
     using C = AttendCfg<D, FP8, QT>;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
     __shared__ uint32_t pages[kChunk + 2];
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                     for (int t = 0; t < QT; ++t) s[t][x] = mfma16x16x32(k, q[t][i], s[t][x]);
                 }
 
-            bf16x8 hi[QT], lo[QT];
+            bf16x8 prob[QT][TERMS];
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
                 float w[8], most = kLowest;
@@ -288,18 +289,26 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
 #pragma unroll
                     for (int i = 0; i < C::DT; ++i) o[t][i] *= f;
                 }
-                uint32_t hb[4], lb[4];
+                uint32_t bits[TERMS][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p0 = exp2_hw(w[2 * i] - m[t]), p1 = exp2_hw(w[2 * i + 1] - m[t]);
-                    l[t] += p0 + p1;
-                    const uint32_t u0 = __float_as_uint(p0) & 0xffff0000u, u1 = __float_as_uint(p1) & 0xffff0000u;
-                    hb[i] = (u0 >> 16) | u1;
-                    const float r0 = fmaxf(p0 - __uint_as_float(u0), 1e-37f), r1 = fmaxf(p1 - __uint_as_float(u1), 1e-37f);
-                    lb[i] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(r0), static_cast<__bf16>(r1)});
+                    float p[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        p[e] = exp2_hw(w[2 * i + e] - m[t]);
+                        l[t] += p[e];
+                    }
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k) {
+                        const uint32_t u0 = __float_as_uint(p[0]) & 0xffff0000u, u1 = __float_as_uint(p[1]) & 0xffff0000u;
+                        bits[k][i] = (u0 >> 16) | u1;
+                        p[0] = fmaxf(p[0] - __uint_as_float(u0), 1e-37f);
+                        p[1] = fmaxf(p[1] - __uint_as_float(u1), 1e-37f);
+                    }
                 }
-                hi[t] = __builtin_bit_cast(bf16x8, u32x4{hb[0], hb[1], hb[2], hb[3]});
-                lo[t] = __builtin_bit_cast(bf16x8, u32x4{lb[0], lb[1], lb[2], lb[3]});
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k)
+                    prob[t][k] = __builtin_bit_cast(bf16x8, u32x4{bits[k][0], bits[k][1], bits[k][2], bits[k][3]});
             }
 
 #pragma unroll
@@ -332,10 +341,9 @@ __global__ __launch_bounds__(256) void attend_kernel(AttendArgs a) {
                     v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
                 }
 #pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                    o[t][i] = mfma16x16x32(v, hi[t], o[t][i]);
-                    o[t][i] = mfma16x16x32(v, lo[t], o[t][i]);
-                }
+                for (int t = 0; t < QT; ++t)
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k) o[t][i] = mfma16x16x32(v, prob[t][k], o[t][i]);
             }
             asm volatile("" ::: "memory");
             __builtin_amdgcn_wave_barrier();
@@ -469,11 +477,14 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 }
 
 // Instantiated here: the launchers below are compiled for the host only.
-#define PROJ_ATTEND_QT(D, QT)                                               \
-    template __global__ void attend_kernel<D, false, QT, false>(AttendArgs); \
-    template __global__ void attend_kernel<D, false, QT, true>(AttendArgs);  \
-    template __global__ void attend_kernel<D, true, QT, false>(AttendArgs);  \
-    template __global__ void attend_kernel<D, true, QT, true>(AttendArgs);
+#define PROJ_ATTEND_AS(D, QT, ONCE, TERMS)                                           \
+    template __global__ void attend_kernel<D, false, QT, ONCE, TERMS>(AttendArgs);  \
+    template __global__ void attend_kernel<D, true, QT, ONCE, TERMS>(AttendArgs);
+#define PROJ_ATTEND_QT(D, QT)         \
+    PROJ_ATTEND_AS(D, QT, false, 2)   \
+    PROJ_ATTEND_AS(D, QT, false, 3)   \
+    PROJ_ATTEND_AS(D, QT, true, 2)    \
+    PROJ_ATTEND_AS(D, QT, true, 3)
 #define PROJ_ATTEND_INST(D) \
     PROJ_ATTEND_QT(D, 1)    \
     template __global__ void attend_join_kernel<D>(AttendArgs);
@@ -530,14 +541,17 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     a.by_die = mixed && a.B * parts >= 8;
     const int64_t grid = a.by_die ? (a.B * parts + 7) / 8 * 8 * (a.c.heads * a.chunks) : rows * parts;
     if (grid > 0x7fffffff || a.B * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
-    auto pick = [&](auto two) {
-        constexpr int QT = decltype(two)::value;
-        if (a.c.fp8) return once ? attend_kernel<D, true, QT, true> : attend_kernel<D, true, QT, false>;
-        return once ? attend_kernel<D, false, QT, true> : attend_kernel<D, false, QT, false>;
+    auto pick = [&](auto two, auto terms) {
+        constexpr int QT = decltype(two)::value, TERMS = decltype(terms)::value;
+        if (a.c.fp8) return once ? attend_kernel<D, true, QT, true, TERMS> : attend_kernel<D, true, QT, false, TERMS>;
+        return once ? attend_kernel<D, false, QT, true, TERMS> : attend_kernel<D, false, QT, false, TERMS>;
     };
-    auto kernel = pick(std::integral_constant<int, 1>());
+    auto pick_terms = [&](auto two) {
+        return a.out_dtype == OUT_F32 ? pick(two, std::integral_constant<int, 3>()) : pick(two, std::integral_constant<int, 2>());
+    };
+    auto kernel = pick_terms(std::integral_constant<int, 1>());
     if constexpr (kTwo)
-        if (qt == 2) kernel = pick(std::integral_constant<int, 2>());
+        if (qt == 2) kernel = pick_terms(std::integral_constant<int, 2>());
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1 || a.join) return e;
