@@ -9,9 +9,10 @@
 
 namespace proj {
 
-// Vector types, not HIP's float2, for what lies in LDS beside the copies' targets: the compiler
-// takes accesses through a struct for possible readers of any copy, and waits for all of them.
-typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
+// For what lies in LDS beside the copies' targets: the compiler takes accesses through types of
+// their own (float, HIP's float2) for possible readers of any copy, and waits for all of them.
+typedef float __attribute__((may_alias)) f32_any;
+typedef uint16_t __attribute__((may_alias)) u16_any;
 
 // Bit position of code j of a word of eight.
 __host__ __device__ constexpr int code_shift(int j) { return 4 * (j / 2) + 16 * (j % 2); }
@@ -343,9 +344,10 @@ struct TileCfg {
     static constexpr int WSTAGE = BN * 64;              // bytes of a step's codes
     static constexpr int NW = WSTAGE / 1024 / WAVES;    // copies of a wave
     static constexpr int SI = (BN * GP + WAVES * 64 - 1) / (WAVES * 64);  // scales of a thread
-    static constexpr int SCALES = GP * BN;              // two floats each
+    static constexpr int SCALES = GP * BN;              // a float and a bf16 each
     static constexpr int SUMS = GP * BM;                // floats
-    static constexpr int LDS = RING * (STAGE + WSTAGE) + 2 * (SCALES * 8 + SUMS * 4);
+    static constexpr int LDS = RING * (STAGE + WSTAGE) + 2 * (SCALES * 6 + SUMS * 4);
+    static_assert(LDS <= 160 << 10, "a compute unit's LDS");
     static_assert(STAGE % (1024 * WAVES) == 0 && WSTAGE % (1024 * WAVES) == 0, "copies divide evenly over the waves");
 };
 
@@ -365,8 +367,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
     constexpr int GP = C::GP, PER = C::PER, THREADS = C::WAVES * 64;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     char *wlds = lds + C::RING * C::STAGE;
-    f32x2 *sc = reinterpret_cast<f32x2 *>(wlds + C::RING * C::WSTAGE);
-    float *sums = reinterpret_cast<float *>(sc + 2 * C::SCALES);
+    float *sums = reinterpret_cast<float *>(wlds + C::RING * C::WSTAGE);
+    f32_any *sc = sums + 2 * C::SUMS;                              // scales [group][column]
+    u16_any *zc = reinterpret_cast<u16_any *>(sc + 2 * C::SCALES);  // 16 + zero point, in bf16
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WM, wn = wave / WM;
 
@@ -458,13 +461,12 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         }
     };
     auto put_scales = [&](int s, int odd) {
-        f32x2 *to = sc + (s & 1) * C::SCALES;
 #pragma unroll
         for (int i = 0; i < C::SI; ++i) {
-            const int e = i * THREADS + tid;
-            const float scale = __uint_as_float(a.scales_f32 ? sv[odd][i] : sv[odd][i] << 16);
-            const float zero = ZEROS ? 16.f + static_cast<float>(zv[odd][i]) : 0.f;
-            if (e < C::SCALES) to[e % GP * C::BN + e / GP] = f32x2{scale, zero};
+            const int e = i * THREADS + tid, to = (s & 1) * C::SCALES + e % GP * C::BN + e / GP;
+            if (e >= C::SCALES) continue;
+            sc[to] = __uint_as_float(a.scales_f32 ? sv[odd][i] : sv[odd][i] << 16);
+            if (ZEROS) zc[to] = f32_to_bf16_bits(16.f + static_cast<float>(zv[odd][i]));
         }
     };
     // LDS offsets of a lane's fragments within a 16-row tile
@@ -547,7 +549,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         lds_wait_all();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        const f32x2 *scs = sc + (s & 1) * C::SCALES + wn * NT * 16 + c16;
+        const int column = (s & 1) * C::SCALES + wn * NT * 16 + c16;
         const float *xs = sums + (s & 1) * C::SUMS + wm * MT * 16 + 4 * g;
         u32x4 w[NT];
 #pragma unroll
@@ -561,10 +563,11 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
             for (int i = 0; i < MT; ++i) cs[i] = *reinterpret_cast<const f32x4 *>(xs + q * C::BM + 16 * i);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const f32x2 sz = scs[q * C::BN + 16 * t];
+                const float scale = sc[column + q * C::BN + 16 * t];
+                const float zero = ZEROS ? bf16_bits_to_f32(zc[column + q * C::BN + 16 * t]) : 0.f;
                 f32x4 p[MT];
 #pragma unroll
-                for (int i = 0; i < MT; ++i) p[i] = ZEROS ? cs[i] * sz[1] : cs[i];
+                for (int i = 0; i < MT; ++i) p[i] = ZEROS ? cs[i] * zero : cs[i];
 #pragma unroll
                 for (int r = q * PER; r < (q + 1) * PER; ++r) {
                     const bf16x8 wf = widen(w[t][r]);
@@ -575,7 +578,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[i][t][v] = __builtin_fmaf(sz[0], p[i][v], acc[i][t][v]);
+                    for (int v = 0; v < 4; ++v) acc[i][t][v] = __builtin_fmaf(scale, p[i][v], acc[i][t][v]);
                 // done here: moved to the step's end, the products of all its groups would be held at once
 #pragma unroll
                 for (int i = 0; i < MT; ++i) asm volatile("" : "+v"(acc[i][t]));
