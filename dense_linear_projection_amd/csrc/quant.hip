@@ -361,7 +361,7 @@ struct TileCfg {
 // the scales and X of s + 3; one barrier a step publishes all of it.  Loads
 // complete in order, so whatever is used a step after its issue makes all that
 // was issued before it wait: everything is used two steps after.
-template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, int EDGE>
+template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool F32, int EDGE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a, int splits) {
     using C = TileCfg<MT, NT, WM, WN, GROUP>;
     constexpr int GP = C::GP, PER = C::PER, THREADS = C::WAVES * 64;
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
     // a row's last step, if it is short, do lanes work out theirs.
     const uint32_t xbytes = static_cast<uint32_t>(rows) * words * 16u, wbytes = static_cast<uint32_t>(cols) * words * 4u;
     const uint32_t G = static_cast<uint32_t>(a.G), sbytes = static_cast<uint32_t>(cols) * G;
-    const uint32_t size = a.scales_f32 ? 4 : 2;
+    constexpr uint32_t size = F32 ? 4 : 2;
     const char *scale0 = static_cast<const char *>(a.scales) + n0 * a.G * size;
     const uint8_t *zero0 = ZEROS ? a.zeros + n0 * a.G : nullptr;
     uint32_t xoff[C::NX], woff[C::NW], soff[C::SI];
@@ -444,7 +444,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         }
     };
     // scales and zero points as they are in memory: converting them waits for them
-    uint32_t sv[2][C::SI], zv[2][C::SI];
+    // (in their own types: so does widening them)
+    std::conditional_t<F32, uint32_t, uint16_t> sv[2][C::SI];
+    uint8_t zv[2][C::SI];
     auto load_scales = [&](int s, int odd) {
         const uint32_t at = static_cast<uint32_t>(first + s) * GP;
         const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(scale0, s < count ? sbytes * size : 0u);
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         for (int i = 0; i < C::SI; ++i) {
             const uint32_t e = i * THREADS + tid;
             const uint32_t off = EDGE == kWhole || GP == 1 || at + e % GP < G ? soff[i] + at : kOutside / 4;
-            if (a.scales_f32)
+            if constexpr (F32)
                 sv[odd][i] = __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(off * 4u), 0, 0);
             else
                 sv[odd][i] = __builtin_amdgcn_raw_buffer_load_b16(rs, static_cast<int>(off * 2u), 0, 0);
@@ -465,7 +467,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         for (int i = 0; i < C::SI; ++i) {
             const int e = i * THREADS + tid, to = (s & 1) * C::SCALES + e % GP * C::BN + e / GP;
             if (e >= C::SCALES) continue;
-            sc[to] = __uint_as_float(a.scales_f32 ? sv[odd][i] : sv[odd][i] << 16);
+            if constexpr (F32)
+                sc[to] = __uint_as_float(sv[odd][i]);
+            else
+                sc[to] = bf16_bits_to_f32(sv[odd][i]);
             if (ZEROS) zc[to] = f32_to_bf16_bits(16.f + static_cast<float>(zv[odd][i]));
         }
     };
@@ -684,16 +689,19 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
 }
 
 // Instantiated here: the launchers below are compiled for the host only.
+#define PROJ_QUANT_TILE(G, Z, F, E)                                                         \
+    template __global__ void quant_tile_kernel<4, 2, 1, 4, G, Z, F, E>(QuantArgs, int);     \
+    template __global__ void quant_tile_kernel<4, 4, 2, 4, G, Z, F, E>(QuantArgs, int);
 #define PROJ_QUANT_EDGE(G, E)                                                               \
     template __global__ void quant_wave_kernel<1, 1, 8, 4, G, E>(QuantArgs, int);           \
     template __global__ void quant_wave_kernel<1, 2, 8, 3, G, E>(QuantArgs, int);           \
     template __global__ void quant_wave_kernel<1, 4, 4, 3, G, E>(QuantArgs, int);           \
     template __global__ void quant_wave_kernel<2, 2, 8, 2, G, E>(QuantArgs, int);           \
     template __global__ void quant_wave_kernel<2, 4, 4, 2, G, E>(QuantArgs, int);           \
-    template __global__ void quant_tile_kernel<4, 2, 1, 4, G, true, E>(QuantArgs, int);     \
-    template __global__ void quant_tile_kernel<4, 2, 1, 4, G, false, E>(QuantArgs, int);    \
-    template __global__ void quant_tile_kernel<4, 4, 2, 4, G, true, E>(QuantArgs, int);     \
-    template __global__ void quant_tile_kernel<4, 4, 2, 4, G, false, E>(QuantArgs, int);
+    PROJ_QUANT_TILE(G, true, true, E)                                                       \
+    PROJ_QUANT_TILE(G, true, false, E)                                                      \
+    PROJ_QUANT_TILE(G, false, true, E)                                                      \
+    PROJ_QUANT_TILE(G, false, false, E)
 #define PROJ_QUANT_GROUP(G)    \
     PROJ_QUANT_EDGE(G, kWhole)  \
     PROJ_QUANT_EDGE(G, kPieces) \
@@ -757,7 +765,8 @@ static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
     if (splits > room) splits = room;
     if (splits < 1) splits = 1;
     if (tiles * splits > 0x7fffffff) return hipErrorInvalidConfiguration;
-    auto kernel = quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, EDGE>;
+    auto kernel = a.scales_f32 ? quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, true, EDGE>
+                               : quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, false, EDGE>;
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                        C::LDS);
     if (e != hipSuccess) return e;
