@@ -25,9 +25,11 @@
 //   * a probability enters as bf16 terms of 8 bits each: for fp32 results three,
 //     which together are its 24 bits; for bf16 results two (48 sequences with a
 //     window: 17.3 us with two, 21.9 with three; two leave fp32 results 4e-6 off
-//     where three leave 3e-7).  They are cut, not rounded, so that what is left
-//     is never negative, and those after the first are at least 1e-37, so that an
-//     infinite value does not meet a zero.
+//     where three leave 3e-7).  All but the last are cut, so that what is left is
+//     never negative; the last is rounded to nearest, so that with two a
+//     probability is off by 2^-17 at most and either way (cut, all were low and
+//     results with them, by 6e-6).  Those after the first are at least 1e-37, so
+//     that an infinite value does not meet a zero.
 //   * K and V are read a KB at a time (whole rows, in the order they lie) into
 //     registers, put into LDS and read from there as the products need them;
 //     those of the next tile are on their way while this one is computed, 16 KB
@@ -302,12 +304,13 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                         l[t] += p[e];
                     }
 #pragma unroll
-                    for (int k = 0; k < TERMS; ++k) {
+                    for (int k = 0; k < TERMS - 1; ++k) {
                         const uint32_t u0 = __float_as_uint(p[0]) & 0xffff0000u, u1 = __float_as_uint(p[1]) & 0xffff0000u;
                         bits[k][i] = (u0 >> 16) | u1;
                         p[0] = fmaxf(p[0] - __uint_as_float(u0), 1e-37f);
                         p[1] = fmaxf(p[1] - __uint_as_float(u1), 1e-37f);
                     }
+                    bits[TERMS - 1][i] = f32_to_bf16_bits(p[0]) | static_cast<uint32_t>(f32_to_bf16_bits(p[1])) << 16;
                 }
 #pragma unroll
                 for (int k = 0; k < TERMS; ++k)
