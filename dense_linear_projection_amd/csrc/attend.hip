@@ -28,8 +28,9 @@
 //     where three leave 3e-7).  All but the last are cut, so that what is left is
 //     never negative; the last is rounded to nearest, so that with two a
 //     probability is off by 2^-17 at most and either way (cut, all were low and
-//     results with them, by 6e-6).  Those after the first are at least 1e-37, so
-//     that an infinite value does not meet a zero.
+//     results with them, by 6e-6).  Those after the first are at least 2^-30 of it,
+//     so that an infinite value does not meet a zero, and zero where it is, so
+//     that a vanished probability takes nothing from a large value.
 //   * K and V are read a KB at a time (whole rows, in the order they lie) into
 //     registers, put into LDS and read from there as the products need them;
 //     those of the next tile are on their way while this one is computed, 16 KB
@@ -297,18 +298,19 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                 uint32_t bits[TERMS][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float p[2];
+                    float p[2], least[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         p[e] = exp2_hw(w[2 * i + e] - m[t]);
                         l[t] += p[e];
+                        least[e] = p[e] * 0x1p-30f;
                     }
 #pragma unroll
                     for (int k = 0; k < TERMS - 1; ++k) {
                         const uint32_t u0 = __float_as_uint(p[0]) & 0xffff0000u, u1 = __float_as_uint(p[1]) & 0xffff0000u;
                         bits[k][i] = (u0 >> 16) | u1;
-                        p[0] = fmaxf(p[0] - __uint_as_float(u0), 1e-37f);
-                        p[1] = fmaxf(p[1] - __uint_as_float(u1), 1e-37f);
+                        p[0] = fmaxf(p[0] - __uint_as_float(u0), least[0]);
+                        p[1] = fmaxf(p[1] - __uint_as_float(u1), least[1]);
                     }
                     bits[TERMS - 1][i] = f32_to_bf16_bits(p[0]) | static_cast<uint32_t>(f32_to_bf16_bits(p[1])) << 16;
                 }

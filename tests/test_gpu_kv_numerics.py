@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+import dense_linear_projection_amd as dlp
 from tests import decode_reference as ref
 from tests.test_gpu_kv import BF16, F32, FP8, make_attend, run_attend
 
@@ -30,3 +31,41 @@ def test_probabilities_are_not_cut_one_way(ctx, dtype):
     w = want[0]
     low = float(((o.cpu().double() - w.to(BF16).double()) / w).mean())
     assert abs(low) < 2.0 ** -18, low
+
+
+def one_head(ctx, K, V, q, n, scale, out):
+    """Results of one sequence of n tokens in one page, one head; K and V [16, 64], q [64]."""
+    cache = dlp.kv_cache(K.view(1, 1, 16, 64).cuda(), V.view(1, 1, 16, 64).cuda())
+    o, e = torch.empty(1, 1, 64, dtype=out, device="cuda"), torch.empty(1, 1, device="cuda")
+    dlp.proj_kv_attend(ctx, cache, q.view(1, 1, 64).cuda(), torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                       torch.tensor([n], dtype=torch.int32, device="cuda"), scale, o, lse=e)
+    return o[0], e[0]
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("low", [-20.0, -60.0, -80.0, -200.0, -3000.0])
+def test_small_probability_of_a_large_value(ctx, out, low):
+    """A value near the type's largest counts by its token's probability, also
+    where that is nothing."""
+    g = torch.Generator().manual_seed(23)
+    K, V, q = torch.zeros(16, 64).to(BF16), torch.randn(16, 64, generator=g).to(BF16), torch.zeros(64).to(BF16)
+    q[0], K[1, 0], V[1] = 1, low, 3e38
+    want, tol = ref.attend(K.view(1, 1, 16, 64), V.view(1, 1, 16, 64), q.view(1, 1, 64), torch.zeros(1, 1, dtype=torch.int32),
+                           torch.tensor([3]), 1.0, 0, (1.0, 1.0), out)
+    if out == BF16:
+        tol[0][...] += 2.0 ** -17 * want[0].abs()      # a probability of 16 bits
+    o, e = one_head(ctx, K, V, q, 3, 1.0, out)
+    ref.close(o[None], want[0], tol[0])
+    ref.close(e[None], want[1], tol[1])
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("low", [0.0, -1.0, -20.0, -60.0])
+def test_infinite_value_inside(ctx, out, low):
+    """An infinite value whose token has a probability gives infinity, of its own sign, and no NaN."""
+    g = torch.Generator().manual_seed(24)
+    K, V, q = torch.zeros(16, 64).to(BF16), torch.randn(16, 64, generator=g).to(BF16), torch.zeros(64).to(BF16)
+    q[0], K[1, 0], V[1, 5], V[1, 6] = 1, low, math.inf, -math.inf
+    o, _ = one_head(ctx, K, V, q, 4, 1.0, out)
+    assert float(o[0, 5]) == math.inf and float(o[0, 6]) == -math.inf
+    assert int(torch.isfinite(o).sum()) == 62
