@@ -5,10 +5,10 @@
 // tokens t of one part of the length,
 //     w[t][h] = scale <q[h], k[t]>,  m = max_t w,  l = sum_t exp(w - m),
 //     o[h][:] = sum_t exp(w[t][h] - m) v[t][:],
-// and parts with (m, l, o) join as (M = max m, sum 2^(m - M) l, ...): one
+// and parts with (m, l, o) join as (M = max m, sum exp(m - M) l, ...): one
 // pass over keys and values, which bound the call (each is read once for
 // `per` query heads: about per operations a byte, far below the matrix
-// cores' rate).  Exponents are kept in base 2.
+// cores' rate).
 //
 // A workgroup is four waves on one (sequence, key-value head, part); wave w
 // takes tiles w, w + 4, ... of 32 tokens, with its own running maximum, sum
@@ -40,8 +40,10 @@
 // Bound by bytes where lengths are large: one sequence of 131072 tokens (8
 // heads of 128 in bf16, 537 MB) 90 us, 6.0 TB/s; 32 sequences up to 16384 tokens
 // 204 us, 5.6 TB/s; by latency where they are small: 500 tokens 8.4 us.
-// The running maximum moves only when a logit passes it by 2^8: sums stay in
-// range, and most tiles need no rescaling and no exchange between lanes.
+// The running maximum moves only when a logit passes it by more than 5 (a
+// factor of 148): sums stay in range, and most tiles need no rescaling and no
+// exchange between lanes.  Logits are kept in natural units, and scaled to base
+// 2 once the maximum is taken off: scaled first, those past 2.36e38 overflowed.
 #include <type_traits>
 
 #include "decode.hpp"
@@ -54,7 +56,8 @@ typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 
 constexpr int kChunk = 2048;       // tokens whose pages are staged at once
 constexpr int kJoined = 32;         // parts that the attention kernel joins itself (500 tokens: 8.0 us, in two kernels 9.3)
-constexpr float kLowest = -3e38f;  // a running maximum before the first logit
+constexpr float kLowest = -0x1.fffffep127f;  // a running maximum before the first logit: the lowest finite one
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Four e4m3 bytes -> bf16, exact; two 32-bit words of pairs.
 __device__ __forceinline__ u32x2 fp8x4_to_bf16(uint32_t w) {
@@ -69,7 +72,8 @@ __device__ __forceinline__ bf16x8 fp8x8_to_bf16(uint32_t lo, uint32_t hi) {
     return __builtin_bit_cast(bf16x8, u32x4{a[0], a[1], b[0], b[1]});
 }
 
-__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+// exp(x - most)
+__device__ __forceinline__ float exp_above(float x, float most) { return __builtin_amdgcn_exp2f((x - most) * kLog2e); }
 
 template <int D, bool FP8, int QT>
 struct AttendCfg {
@@ -118,7 +122,7 @@ __device__ __forceinline__ void finish_head(const AttendArgs &a, int64_t at, int
         *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.out) + at) = u32x2{lo, hi};
     }
     if (d == 0 && a.lse)
-        a.lse[row] = total == 0.f ? -__builtin_inff() : (most + log2f(total)) * 0.6931471805599453f;
+        a.lse[row] = total == 0.f ? -__builtin_inff() : most + __builtin_amdgcn_logf(total) * 0.6931471805599453f;
 }
 
 // Two floats of a part's result: through the device's memory where another
@@ -191,7 +195,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
     const char *kb = static_cast<const char *>(a.c.k) + h * a.c.kh * (FP8 ? 1 : 2);
     const char *vb = static_cast<const char *>(a.c.v) + h * a.c.vh * (FP8 ? 1 : 2);
     const int64_t place_mask = (int64_t{1} << a.c.page_shift) - 1;
-    const float to_exp2 = a.scale * a.c.k_scale * 1.4426950408889634f;
+    const float to_logit = a.scale * a.c.k_scale;
     char *kt = lds + wave * 2 * C::TILE, *vt = kt + C::TILE;
     u32x4 kr[C::VI], vr[C::VI];
 
@@ -282,14 +286,14 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                 float w[8], most = kLowest;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    w[i] = s[t][i / 4][i % 4] * to_exp2;
+                    w[i] = s[t][i / 4][i % 4] * to_logit;
                     if (!whole && 32 * j + 16 * (i / 4) + 4 * g + i % 4 >= left) w[i] = -__builtin_inff();
                     most = fmaxf(most, w[i]);
                 }
-                if (__any(most > m[t] + 8.f)) {
+                if (__any(most > m[t] + 5.f)) {
                     most = fmaxf(most, __shfl_xor(most, 16, 64));
                     most = fmaxf(fmaxf(most, __shfl_xor(most, 32, 64)), m[t]);
-                    const float f = exp2_hw(m[t] - most);
+                    const float f = exp_above(m[t], most);
                     m[t] = most;
                     l[t] *= f;
 #pragma unroll
@@ -301,7 +305,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                     float p[2], least[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        p[e] = exp2_hw(w[2 * i + e] - m[t]);
+                        p[e] = exp_above(w[2 * i + e], m[t]);
                         l[t] += p[e];
                         least[e] = p[e] * 0x1p-30f;
                     }
@@ -383,7 +387,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const float f = exp2_hw(top[w][hq] - most);
+                const float f = exp_above(top[w][hq], most);
                 total += f * sum[w][hq];
                 v += *reinterpret_cast<const f32x4 *>(red + (w * 16 + hq) * (D + 4) + d) * f;
             }
@@ -433,7 +437,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
         for (int p = 0; p < parts; ++p) {
             const float *x = from + p * (D + 4);
             const float2 ml = get_part(x + D), lo = get_part(x + d), hi = get_part(x + d + 2);
-            const float f = exp2_hw(ml.x - most);
+            const float f = exp_above(ml.x, most);
             total += ml.y * f;
             v += f32x4{lo.x, lo.y, hi.x, hi.y} * f;
         }
@@ -465,7 +469,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         float total = 0.f;
         for (int p = slice; p < parts; p += SLICES) {
             const float *x = from + static_cast<int64_t>(p) * (D + 4);
-            const float f = exp2_hw(x[D] - most);
+            const float f = exp_above(x[D], most);
             v += *reinterpret_cast<const f32x4 *>(x + d) * f;
             total += x[D + 1] * f;
         }

@@ -69,3 +69,36 @@ def test_infinite_value_inside(ctx, out, low):
     o, _ = one_head(ctx, K, V, q, 4, 1.0, out)
     assert float(o[0, 5]) == math.inf and float(o[0, 6]) == -math.inf
     assert int(torch.isfinite(o).sum()) == 62
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("logit", [-2.4e38, -3.38e38, 2.0e38, 2.4e38, 3.38e38])
+def test_logits_near_the_largest(ctx, out, logit):
+    """Every finite logit counts: tokens that all have the same share alike,
+    one above the others takes all, however far from zero they are."""
+    g = torch.Generator().manual_seed(25)
+    K, V, q = torch.zeros(16, 64).to(BF16), torch.randn(16, 64, generator=g).to(BF16), torch.zeros(64).to(BF16)
+    q[0], K[:, 0] = 1, logit
+    o, e = one_head(ctx, K, V, q, 7, 1.0, out)
+    mean = V[:7].double().mean(0)
+    # seven equal probabilities: each fp32 sum's roundings, and the result's own
+    ref.close(o[0], mean, 16 * ref.EPS32 * V[:7].double().abs().mean(0) + ref.HALF[out] * mean.abs())
+    assert abs(float(e) / float(K[0, 0]) - 1) < 2 * ref.EPS32
+    if logit < 0:
+        K[5, 0] = 0
+        o, e = one_head(ctx, K, V, q, 7, 1.0, out)
+        assert torch.equal(o[0].cpu(), V[5].to(out)) and float(e) == 0
+    K[:, 0], K[2, 0] = -logit, logit
+    o, e = one_head(ctx, K, V, q, 7, 1.0, out)
+    rest = [i for i in range(7) if i != 2]
+    want = V[2].double() if logit > 0 else V[rest].double().mean(0)
+    ref.close(o[0], want, 16 * ref.EPS32 * V[:7].double().abs().amax(0) + ref.HALF[out] * want.abs())
+
+
+def test_large_negative_scale(ctx):
+    """A negative scale turns the order of the logits round."""
+    k, v, cache, q, tables, n, scales = make_attend(3, 8, 2, 64, 16, BF16, "hnd", [300, 17, 64], 26)
+    want, tol = ref.attend(k, v, q, tables, n, -1.5, 0, scales, F32)
+    o, e = run_attend(ctx, cache, q, tables, n, -1.5, F32)
+    ref.close(o, want[0], tol[0])
+    ref.close(e, want[1], tol[1])
