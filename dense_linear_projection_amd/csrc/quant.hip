@@ -22,6 +22,37 @@ __device__ __forceinline__ float group_scale(const QuantArgs &a, int64_t i) {
                         : bf16_bits_to_f32(static_cast<const uint16_t *>(a.scales)[i]);
 }
 
+constexpr float kLargest = 0x1.fffffep127f;
+
+// Words w0 .. w1 - 1 of one output by the definition, x times s (c - z).  The
+// kernels below put this in the place of a sum that is not finite: they take
+// a group's scale, the matrix cores also 16 + z times its sum of x, after the
+// sum over x c, so that an infinite x and sums beyond the largest number give
+// NaN or infinity where the definition has infinity or a number.  One lane's
+// work, since such an X is a fault or an extreme: K = N = 8192 with an infinity in
+// one of 16 rows 420 us instead of 13, in each of 1024 rows 50 ms instead of 0.16
+// (a NaN ends the walk: 0.2).
+__device__ __forceinline__ float quant_by_definition(int64_t m, int64_t n, int64_t w0, int64_t w1) {
+    // The call's arguments (every kernel's first), read again: kept for this, they would take registers from the loops.
+    auto kernarg = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(kernarg));
+    const QuantArgs &a = *(const QuantArgs *)kernarg;
+    const int64_t words = a.K / 8;
+    float acc = 0.f;
+#pragma unroll 1
+    for (int64_t w = w0; w < w1 && acc == acc; ++w) {  // NaN stays
+        const uint32_t word = a.codes[n * words + w];
+        const int64_t g = n * a.G + w * 8 / a.group;
+        const float z = a.zeros ? static_cast<float>(a.zeros[g]) : 8.f, s = group_scale(a, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float c = static_cast<float>((word >> code_shift(j)) & 15u);
+            acc = __builtin_fmaf(bf16_bits_to_f32(a.X[m * a.K + w * 8 + j]), s * (c - z), acc);
+        }
+    }
+    return acc;
+}
+
 // Any K (a multiple of 8) and alignment: one wave per output, lane l taking
 // words l, l + 64, ... of the row.  A word lies within one group.
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
@@ -45,6 +76,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
 #pragma unroll
     for (int h = 32; h >= 1; h >>= 1) acc += __shfl_xor(acc, h, 64);
     if (lane == 0) {
+        if (!(fabsf(acc) <= kLargest)) acc = quant_by_definition(m, n, 0, words);
         const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n]) : 0.f;
         store_out(a.Y, a.out, idx, apply_epilogue(acc, a.epi, b));
     }
@@ -313,8 +345,16 @@ __global__ __launch_bounds__(WAVES * 64) void quant_wave_kernel(QuantArgs a, int
         }
     }
 
-    // add the waves' sums, 16 rows at a time, over their pieces of LDS (1 KB for each tile of columns)
+    // add the waves' sums, 16 rows at a time, over their pieces of LDS (1 KB for each tile of columns); those
+    // that are not finite are marked and done again at the end, where their code is not in the way
     float *red = reinterpret_cast<float *>(lds);
+    constexpr int EACH = (16 * COLS + THREADS - 1) / THREADS;  // outputs of a thread of 16 rows
+    static_assert(MT * EACH <= 32, "a bit to a sum");
+    uint32_t again = 0;
+    auto put = [&](int m, int n, float y) {
+        const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n0 + n]) : 0.f;
+        store_out(a.Y, a.out, m * a.N + n0 + n, apply_epilogue(y, a.epi, b));
+    };
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         __syncthreads();
@@ -324,15 +364,22 @@ __global__ __launch_bounds__(WAVES * 64) void quant_wave_kernel(QuantArgs a, int
             for (int v = 0; v < 4; ++v) red[(wave * 16 + 4 * g + v) * COLS + 16 * t + c16] = acc[i][t][v];
         __syncthreads();
         const int rows = M - 16 * i < 16 ? M - 16 * i : 16;
-        for (int e = tid; e < rows * COLS; e += THREADS) {
+        for (int e = tid, k = 0; e < rows * COLS; e += THREADS, ++k) {
             const int m = e / COLS, n = e % COLS;
             if (n >= cols) continue;
             float y = 0.f;
 #pragma unroll
-            for (int k = 0; k < WAVES; ++k) y += red[(k * 16 + m) * COLS + n];
-            const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n0 + n]) : 0.f;
-            store_out(a.Y, a.out, (16 * i + m) * a.N + n0 + n, apply_epilogue(y, a.epi, b));
+            for (int w = 0; w < WAVES; ++w) y += red[(w * 16 + m) * COLS + n];
+            if (fabsf(y) <= kLargest)
+                put(16 * i + m, n, y);
+            else
+                again |= 1u << (i * EACH + k);
         }
+    }
+    if (!__any(again != 0)) return;
+    for (; again != 0; again &= again - 1) {
+        const int bit = __builtin_ctz(again), e = tid + bit % EACH * THREADS, m = bit / EACH * 16 + e / COLS, n = e % COLS;
+        put(m, n, quant_by_definition(m, n0 + n, 0, words));
     }
 }
 
@@ -621,23 +668,46 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
     }
     wait_vm<0>();
 
+    // Sums that are not finite are marked, and done again one after the other:
+    // in place, their code would be there once for every sum.  The lane's place
+    // is worked out again, so that it takes no registers in the loop.
+    int l = static_cast<int>(__lane_id());
+    asm volatile("" : "+v"(l));
+    const int row0 = wm * MT * 16 + 4 * (l >> 4), col0 = wn * NT * 16 + (l & 15);
+    auto put = [&](int r, int col, float sum, float b) {
+        const int64_t at = (m0 + r) * a.N + n0 + col;
+        if (splits > 1)
+            a.ws[split * a.M * a.N + at] = sum;
+        else
+            store_out(a.Y, a.out, at, apply_epilogue(sum, a.epi, b));
+    };
+    const bool biased = (a.epi & 1) && splits == 1;
+    uint64_t again = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int col = (wn * NT + t) * 16 + c16;
+        const int col = col0 + 16 * t;
         if (col >= cols) continue;
-        const float b = (a.epi & 1) && splits == 1 ? bf16_bits_to_f32(a.bias[n0 + col]) : 0.f;
+        const float b = biased ? bf16_bits_to_f32(a.bias[n0 + col]) : 0.f;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int r = (wm * MT + i) * 16 + 4 * g + v;
+                const int r = row0 + 16 * i + v;
                 if (r >= rows) continue;
-                const int64_t at = (m0 + r) * a.N + n0 + col;
-                if (splits > 1)
-                    a.ws[split * a.M * a.N + at] = acc[i][t][v];
+                if (fabsf(acc[i][t][v]) <= kLargest)
+                    put(r, col, acc[i][t][v], b);
                 else
-                    store_out(a.Y, a.out, at, apply_epilogue(acc[i][t][v], a.epi, b));
+                    again |= uint64_t{1} << ((t * MT + i) * 4 + v);
             }
+    }
+    static_assert(NT * MT * 4 <= 64, "a bit to a sum");
+    const int64_t w0 = static_cast<int64_t>(first) * 16, w1 = w0 + static_cast<int64_t>(count) * 16;
+    if (!__any(again != 0)) return;
+    for (; again != 0; again &= again - 1) {
+        const int bit = __builtin_ctzll(again), v = bit & 3, i = (bit >> 2) % MT, t = (bit >> 2) / MT;
+        const int r = row0 + 16 * i + v, col = col0 + 16 * t;
+        put(r, col, quant_by_definition(m0 + r, n0 + col, w0, w1 < words ? w1 : words),
+            biased ? bf16_bits_to_f32(a.bias[n0 + col]) : 0.f);
     }
 }
 

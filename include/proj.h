@@ -286,7 +286,11 @@ proj_status proj_quantize_weights(proj_ctx *ctx, const void *W, int64_t N, int64
  * Epilogue, output types, M = 0, N = 0, K = 0 and overlap rules as proj_run.
  * Products of X with the codes are exact, sums are fp32, the scales are
  * applied to the fp32 sums of a group: nothing is rounded to bf16 before the
- * output.  A NaN or an infinity in X makes its row's results NaN.  Allocates nothing and never synchronises, so it may be captured;
+ * output.  A NaN in X makes its row's results NaN.  An infinity gives what the
+ * formula gives (an infinity, or NaN where its weight is 0 or another has the
+ * other sign), and so do sums that pass the largest float before their scale is
+ * applied: such outputs are worked out one by one, 50 ms for 1024 x 8192 of them
+ * at K = 8192.  Allocates nothing and never synchronises, so it may be captured;
  * which kernel runs follows from sizes and alignment alone (no tuning, no
  * plan), so the same call gives the same bits every time.  Codes that are not
  * 4-byte aligned, scales or X not aligned to their type: PROJ_ERR_INVALID_ARG. */

@@ -1,0 +1,71 @@
+"""4-bit projection where numbers end: infinities and NaN in X, sums that pass
+the largest float on their way, X of one sign, on every kernel and alignment,
+against the definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from tests import decode_reference as ref
+from tests.test_gpu_quant import BF16, F32, make, run
+
+pytestmark = pytest.mark.gpu
+
+# rows, columns, K: waves over K, small tiles, small tiles split over K, large tiles; each with whole and ragged steps
+SHAPES = [(1, 70, 1024), (5, 70, 1000), (20, 100, 1024), (40, 300, 512), (40, 70, 2056), (64, 130, 8192), (600, 7000, 264)]
+
+
+def bound(X, codes, scales, group, K):
+    """At most 47 |x| s a term, every one of them rounded on its way, and the sum's own."""
+    size = 47.0 * (X.double().abs() @ scales.double().abs()[:, torch.arange(K) // group].t())
+    return ref.EPS32 * size
+
+
+def by_definition(X, codes, scales, z, group):
+    """The products summed one by one where X has infinities: torch's product gives those no fixed meaning."""
+    W = ref.weights(codes, scales, z, group)
+    return torch.stack([(x[None] * W).sum(1) for x in X.double()])
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_infinities(ctx, M, N, K, group, offset):
+    """An infinite x gives infinity, of the sign of its weight, or NaN where the
+    weight is zero or a second one has the other sign; its row alone."""
+    for zeros, sdt in ((True, BF16), (False, F32)):
+        X, codes, scales, z, _ = make(M, N, K, group, zeros, sdt, False, M + N + K + group)
+        want, tol = ref.quant(X, codes, scales, z, group, None, 0, F32)
+        odd = sorted({0, M // 2, M - 1})
+        X[odd[0], K - 3] = math.inf
+        X[odd[-1], 5] = -math.inf
+        X[odd[len(odd) // 2], K // 2], X[odd[len(odd) // 2], 9] = math.inf, math.inf
+        want[odd], tol[odd] = by_definition(X[odd], codes, scales, z, group), 0.0
+        got = run(ctx, X, codes, scales, z, group, None, 0, F32, offset=offset)
+        assert 0 < int(torch.isinf(want).sum())
+        ref.close(got, want, tol)
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES[:-1])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_sums_that_pass_the_largest_float(ctx, M, N, K, offset):
+    """X of 3e37: times 16 + 15 a code, or a group of them, it is past the
+    largest float; times the weights, about 1e-6, it is not."""
+    for zeros, sdt, group in ((True, BF16, 64), (False, F32, 32)):
+        X, codes, scales, z, _ = make(M, N, K, group, zeros, sdt, False, M + K)
+        X = (X.sign() * 3e37).to(BF16)
+        scales = (scales.double() * 1e-6).to(sdt)
+        want = X.double() @ ref.weights(codes, scales, z, group).t()
+        got = run(ctx, X, codes, scales, z, group, None, 0, F32, offset=offset)
+        ref.close(got, want, 8 * bound(X, codes, scales, group, K))
+
+
+@pytest.mark.parametrize("M", [1, 20, 64, 300])
+def test_epilogue_of_infinities(ctx, M):
+    """Bias and output type apply to an infinity as to a number."""
+    X, codes, scales, z, b = make(M, 100, 512, 64, True, BF16, True, M)
+    X[0, 77] = math.inf
+    want = by_definition(X[:1], codes, scales, z, 64) + b.double()
+    for out in (F32, BF16):
+        got = run(ctx, X, codes, scales, z, 64, b, 1, out)[:1]
+        ref.close(got, want, torch.zeros_like(want))
