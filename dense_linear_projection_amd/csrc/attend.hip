@@ -522,7 +522,21 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     constexpr bool kTwo = D <= 128;
     const int per = a.q_heads / a.c.heads, qt = kTwo && per > 16 ? 2 : 1;
     a.chunks = (per + 16 * qt - 1) / (16 * qt);
-    const int64_t rows = a.B * a.c.heads * a.chunks;
+    const int64_t hh = static_cast<int64_t>(a.c.heads) * a.chunks, rows = a.B * hh, most_rows = most_groups(256) - 7 * hh;
+    if (a.B > 1 && (rows > most_rows || a.B * a.q_heads > most_groups(256))) {
+        // more than one launch can have workgroups for: half the sequences at a time
+        AttendArgs x = a, y = a;
+        x.B = a.B / 2;
+        y.B = a.B - x.B;
+        y.q = a.q + x.B * a.q_stride;
+        y.tables = a.tables + x.B * a.table_stride;
+        y.lengths = a.lengths + x.B;
+        const int64_t heads = x.B * a.q_heads;
+        y.out = static_cast<char *>(a.out) + heads * D * (a.out_dtype == OUT_F32 ? 4 : 2);
+        y.lse = a.lse ? a.lse + heads : nullptr;
+        const hipError_t e = launch_attend_dim<D>(x, st);
+        return e != hipSuccess ? e : launch_attend_dim<D>(y, st);
+    }
     const int64_t span = a.window > 0 && a.window < a.max_len ? a.window : a.max_len;
     // Parts of the length: enough workgroups for four to a compute unit, none
     // shorter than one tile for each wave, and none so long that units idle at
@@ -532,7 +546,9 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     int64_t part = (span * rows + want - 1) / want;
     part = part < 128 ? 128 : part > most ? most : (part + 127) / 128 * 128;
     int64_t parts = span > part ? (span + part - 1) / part : 1;
-    const int64_t room = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
+    // no more than the workspace holds and one launch can have
+    const int64_t held = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
+    const int64_t room = held < most_rows / rows ? held : most_rows / rows;
     if (parts > 1 && parts > room) {
         parts = room < 1 ? 1 : room;
         part = ((span + parts - 1) / parts + 127) / 128 * 128;
@@ -551,8 +567,7 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     const bool once = !mixed || (D * size % 128 == 0 && (a.c.kt | a.c.vt | a.c.kh | a.c.vh) * size % 128 == 0 &&
                                  (reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v)) % 128 == 0);
     a.by_die = mixed && a.B * parts >= 8;
-    const int64_t grid = a.by_die ? (a.B * parts + 7) / 8 * 8 * (a.c.heads * a.chunks) : rows * parts;
-    if (grid > 0x7fffffff || a.B * a.q_heads > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const int64_t grid = a.by_die ? (a.B * parts + 7) / 8 * 8 * hh : rows * parts;
     auto pick = [&](auto two, auto terms) {
         constexpr int QT = decltype(two)::value, TERMS = decltype(terms)::value;
         if (a.c.fp8) return once ? attend_kernel<D, true, QT, true, TERMS> : attend_kernel<D, true, QT, false, TERMS>;

@@ -6,6 +6,11 @@
 
 namespace proj {
 
+// Workgroups that one launch may have: HIP takes less than 2^32 threads and 2^31 workgroups.
+constexpr int64_t most_groups(int threads) {
+    return 0xffffffffll / threads < 0x7fffffff ? 0xffffffffll / threads : 0x7fffffff;
+}
+
 // One call of the 4-bit projection.
 struct QuantArgs {
     const uint16_t *X;      // bf16 [M, K]

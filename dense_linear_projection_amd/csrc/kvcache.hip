@@ -171,11 +171,22 @@ static hipError_t launch_append_as(const AppendArgs &a, hipStream_t st) {
     const int64_t blocks = (items + 255) / 256;
     // four tokens to a thread once that leaves enough threads for the chip
     const int tok = a.T * items >= (int64_t{1} << 20) ? 4 : 1;
-    const int64_t grid = (a.T + tok - 1) / tok * blocks;
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
     auto kernel = tok == 4 ? append_kernel<PAIRING, 4> : append_kernel<PAIRING, 1>;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a, static_cast<uint32_t>(blocks));
-    return hipGetLastError();
+    // as many tokens at a time as one launch can have threads for
+    const int64_t most = most_groups(256) / blocks * tok;
+    AppendArgs s = a;
+    for (int64_t t = 0; t < a.T; t += most) {
+        s.T = a.T - t < most ? a.T - t : most;
+        s.qkv = a.qkv + t * a.stride;
+        s.positions = a.positions + t;
+        s.slots = a.slots + t;
+        s.q_out = a.q_out ? a.q_out + t * a.q_heads * a.c.dim : nullptr;
+        const int64_t grid = (s.T + tok - 1) / tok * blocks;
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, s, static_cast<uint32_t>(blocks));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_append(const AppendArgs &a, hipStream_t st) {

@@ -53,32 +53,35 @@ __device__ __forceinline__ float quant_by_definition(int64_t m, int64_t n, int64
     return acc;
 }
 
-// Any K (a multiple of 8) and alignment: one wave per output, lane l taking
-// words l, l + 64, ... of the row.  A word lies within one group.
+// Any K (a multiple of 8), alignment and number of outputs: one wave per
+// output, lane l taking words l, l + 64, ... of the row.  A word lies within
+// one group.  A launch that cannot have a wave for every output goes round.
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
     const int lane = threadIdx.x & 63;
-    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (idx >= a.M * a.N) return;
-    const int64_t m = idx / a.N, n = idx % a.N, words = a.K / 8;
-    float acc = 0.f;
-    for (int64_t w = lane; w < words; w += 64) {
-        const uint32_t word = a.codes[n * words + w];
-        const int64_t g = n * a.G + w * 8 / a.group;
-        const float z = a.zeros ? static_cast<float>(a.zeros[g]) : 8.f;
-        float s = 0.f;
+    const int64_t words = a.K / 8, outputs = a.M * a.N;
+    for (int64_t idx = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); idx < outputs;
+         idx += static_cast<int64_t>(gridDim.x) * 4) {
+        const int64_t m = idx / a.N, n = idx % a.N;
+        float acc = 0.f;
+        for (int64_t w = lane; w < words; w += 64) {
+            const uint32_t word = a.codes[n * words + w];
+            const int64_t g = n * a.G + w * 8 / a.group;
+            const float z = a.zeros ? static_cast<float>(a.zeros[g]) : 8.f;
+            float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float c = static_cast<float>((word >> code_shift(j)) & 15u);
-            s = __builtin_fmaf(bf16_bits_to_f32(a.X[m * a.K + w * 8 + j]), c - z, s);
+            for (int j = 0; j < 8; ++j) {
+                const float c = static_cast<float>((word >> code_shift(j)) & 15u);
+                s = __builtin_fmaf(bf16_bits_to_f32(a.X[m * a.K + w * 8 + j]), c - z, s);
+            }
+            acc = __builtin_fmaf(s, group_scale(a, g), acc);
         }
-        acc = __builtin_fmaf(s, group_scale(a, g), acc);
-    }
 #pragma unroll
-    for (int h = 32; h >= 1; h >>= 1) acc += __shfl_xor(acc, h, 64);
-    if (lane == 0) {
-        if (!(fabsf(acc) <= kLargest)) acc = quant_by_definition(m, n, 0, words);
-        const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n]) : 0.f;
-        store_out(a.Y, a.out, idx, apply_epilogue(acc, a.epi, b));
+        for (int h = 32; h >= 1; h >>= 1) acc += __shfl_xor(acc, h, 64);
+        if (lane == 0) {
+            if (!(fabsf(acc) <= kLargest)) acc = quant_by_definition(m, n, 0, words);
+            const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[n]) : 0.f;
+            store_out(a.Y, a.out, idx, apply_epilogue(acc, a.epi, b));
+        }
     }
 }
 
@@ -712,12 +715,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
 }
 
 __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *q, int64_t words, uint32_t *codes) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= words) return;
-    uint32_t w = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < words;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        uint32_t w = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w |= static_cast<uint32_t>(q[i * 8 + j] & 15) << code_shift(j);
-    codes[i] = w;
+        for (int j = 0; j < 8; ++j) w |= static_cast<uint32_t>(q[i * 8 + j] & 15) << code_shift(j);
+        codes[i] = w;
+    }
 }
 
 // One wave per group of a row: the group's extremes, then its codes.  Lane l
@@ -725,40 +729,41 @@ __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *q, int64
 __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_t N, int64_t K, int64_t G, int group,
                                                        uint32_t *codes, void *scales, int scales_f32, uint8_t *zeros) {
     const int lane = threadIdx.x & 63;
-    const int64_t idx = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (idx >= N * G) return;
-    const int64_t n = idx / G, k = (idx % G) * group + lane * 8;
-    const bool live = lane * 8 < group && k < K;
-    float w[8], lo = 0.f, hi = 0.f;
+    for (int64_t idx = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); idx < N * G;
+         idx += static_cast<int64_t>(gridDim.x) * 4) {
+        const int64_t n = idx / G, k = (idx % G) * group + lane * 8;
+        const bool live = lane * 8 < group && k < K;
+        float w[8], lo = 0.f, hi = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        w[j] = live ? bf16_bits_to_f32(W[n * K + k + j]) : 0.f;
-        lo = fminf(lo, w[j]);
-        hi = fmaxf(hi, w[j]);
-    }
+        for (int j = 0; j < 8; ++j) {
+            w[j] = live ? bf16_bits_to_f32(W[n * K + k + j]) : 0.f;
+            lo = fminf(lo, w[j]);
+            hi = fmaxf(hi, w[j]);
+        }
 #pragma unroll
-    for (int h = 32; h >= 1; h >>= 1) {
-        lo = fminf(lo, __shfl_xor(lo, h, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, h, 64));
-    }
-    float s = zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
-    if (!scales_f32) s = bf16_bits_to_f32(f32_to_bf16_bits(s));
-    const float z = !zeros ? 8.f : s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
-    if (lane == 0) {
-        if (scales_f32)
-            static_cast<float *>(scales)[idx] = s;
-        else
-            static_cast<uint16_t *>(scales)[idx] = f32_to_bf16_bits(s);
-        if (zeros) zeros[idx] = static_cast<uint8_t>(z);
-    }
-    if (!live) return;
-    uint32_t word = 0;
+        for (int h = 32; h >= 1; h >>= 1) {
+            lo = fminf(lo, __shfl_xor(lo, h, 64));
+            hi = fmaxf(hi, __shfl_xor(hi, h, 64));
+        }
+        float s = zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+        if (!scales_f32) s = bf16_bits_to_f32(f32_to_bf16_bits(s));
+        const float z = !zeros ? 8.f : s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
+        if (lane == 0) {
+            if (scales_f32)
+                static_cast<float *>(scales)[idx] = s;
+            else
+                static_cast<uint16_t *>(scales)[idx] = f32_to_bf16_bits(s);
+            if (zeros) zeros[idx] = static_cast<uint8_t>(z);
+        }
+        if (!live) continue;
+        uint32_t word = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float c = s > 0.f ? fminf(fmaxf(rintf(w[j] / s) + z, 0.f), 15.f) : z;
-        word |= static_cast<uint32_t>(c) << code_shift(j);
+        for (int j = 0; j < 8; ++j) {
+            const float c = s > 0.f ? fminf(fmaxf(rintf(w[j] / s) + z, 0.f), 15.f) : z;
+            word |= static_cast<uint32_t>(c) << code_shift(j);
+        }
+        codes[(n * K + k) / 8] = word;
     }
-    codes[(n * K + k) / 8] = word;
 }
 
 // Instantiated here: the launchers below are compiled for the host only.
@@ -782,18 +787,22 @@ PROJ_QUANT_GROUP(64)
 PROJ_QUANT_GROUP(128)
 
 #ifndef __HIP_DEVICE_COMPILE__
-static bool grid_for(int64_t items, int64_t per, unsigned *grid) {
+// Workgroups of 256 threads for kernels that go round where these are too few.
+static dim3 grid_for(int64_t items, int64_t per) {
     const int64_t g = (items + per - 1) / per;
-    if (g <= 0 || g > 0x7fffffff) return false;
-    *grid = static_cast<unsigned>(g);
-    return true;
+    return dim3(static_cast<unsigned>(g < most_groups(256) ? g : most_groups(256)));
+}
+
+static hipError_t launch_rows(const QuantArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL(quant_rows_kernel, grid_for(a.M * a.N, 4), dim3(256), 0, st, a);
+    return hipGetLastError();
 }
 
 template <int MT, int NT, int WAVES, int DEPTH, int GROUP, int EDGE>
 static hipError_t run_wave(const QuantArgs &a, hipStream_t st) {
-    unsigned grid;
-    if (!grid_for(a.N, 16 * NT, &grid)) return hipErrorInvalidConfiguration;
     constexpr int gp = 128 / GROUP, cols = 16 * NT;
+    const int64_t groups_n = (a.N + cols - 1) / cols;
+    if (groups_n > most_groups(WAVES * 64)) return launch_rows(a, st);
     // the waves' own pieces, and the scales of as many steps as fit into 44 KB
     // beside them: 5 bytes a group, rows padded
     constexpr int pieces = WAVES * (NT * 1024 + MT * 4096);
@@ -809,7 +818,8 @@ static hipError_t run_wave(const QuantArgs &a, hipStream_t st) {
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(WAVES * 64), static_cast<unsigned>(lds), st, a, static_cast<int>(span));
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups_n)), dim3(WAVES * 64), static_cast<unsigned>(lds), st, a,
+                       static_cast<int>(span));
     return hipGetLastError();
 }
 
@@ -839,7 +849,7 @@ static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
     const int64_t room = static_cast<int64_t>(a.ws_bytes / 4) / (a.M * a.N);
     if (splits > room) splits = room;
     if (splits < 1) splits = 1;
-    if (tiles * splits > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (tiles * splits > most_groups(C::WAVES * 64)) return launch_rows(a, st);
     auto kernel = a.scales_f32 ? quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, true, EDGE>
                                : quant_tile_kernel<MT, NT, WM, WN, GROUP, ZEROS, false, EDGE>;
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -891,25 +901,18 @@ hipError_t launch_quant(const QuantArgs &args, hipStream_t st) {
             case 128: return launch_edge<128>(a, st);
         }
     }
-    unsigned grid;
-    if (!grid_for(a.M * a.N, 4, &grid)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(quant_rows_kernel, dim3(grid), dim3(256), 0, st, a);
-    return hipGetLastError();
+    return launch_rows(a, st);
 }
 
 hipError_t launch_pack_codes(const uint8_t *q, int64_t N, int64_t K, uint32_t *codes, hipStream_t st) {
-    unsigned grid;
-    if (!grid_for(N * K / 8, 256, &grid)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(pack_codes_kernel, dim3(grid), dim3(256), 0, st, q, N * K / 8, codes);
+    hipLaunchKernelGGL(pack_codes_kernel, grid_for(N * K / 8, 256), dim3(256), 0, st, q, N * K / 8, codes);
     return hipGetLastError();
 }
 
 hipError_t launch_quantize(const uint16_t *W, int64_t N, int64_t K, int group, uint32_t *codes, void *scales,
                            int scales_f32, uint8_t *zeros, hipStream_t st) {
     const int64_t G = (K + group - 1) / group;
-    unsigned grid;
-    if (!grid_for(N * G, 4, &grid)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(quantize_kernel, dim3(grid), dim3(256), 0, st, W, N, K, G, group, codes, scales, scales_f32,
+    hipLaunchKernelGGL(quantize_kernel, grid_for(N * G, 4), dim3(256), 0, st, W, N, K, G, group, codes, scales, scales_f32,
                        zeros);
     return hipGetLastError();
 }
