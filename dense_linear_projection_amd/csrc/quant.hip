@@ -734,11 +734,13 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
         const int64_t n = idx / G, k = (idx % G) * group + lane * 8;
         const bool live = lane * 8 < group && k < K;
         float w[8], lo = 0.f, hi = 0.f;
+        bool finite = true;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             w[j] = live ? bf16_bits_to_f32(W[n * K + k + j]) : 0.f;
             lo = fminf(lo, w[j]);
             hi = fmaxf(hi, w[j]);
+            finite = finite && fabsf(w[j]) <= kLargest;
         }
 #pragma unroll
         for (int h = 32; h >= 1; h >>= 1) {
@@ -747,6 +749,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
         }
         float s = zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
         if (!scales_f32) s = bf16_bits_to_f32(f32_to_bf16_bits(s));
+        if (__any(!finite)) s = __builtin_nanf("");  // the extremes above leave a NaN out
         const float z = !zeros ? 8.f : s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
         if (lane == 0) {
             if (scales_f32)

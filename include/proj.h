@@ -276,7 +276,8 @@ proj_status proj_run_candidate_packed(proj_ctx *ctx, int index, const void *X, c
  * W [N][K]: with zeros, lo = min(0, min W), hi = max(0, max W) of the group,
  * s = (hi - lo) / 15 rounded to the scales' type, z = rint(-lo / s),
  * c = rint(W / s) + z; without (zeros NULL), s = max|W| / 7 and z = 8; both
- * clamped to 0..15, a group of zeros having s = 0 and c = z.  Every
+ * clamped to 0..15, a group of zeros having s = 0 and c = z, one with a NaN or an
+ * infinity s = NaN (its weights all are).  Every
  * operand stays owned by the caller; N = 0 or K = 0 is a no-op. */
 proj_status proj_pack_codes(proj_ctx *ctx, const uint8_t *q, int64_t N, int64_t K, uint32_t *codes, void *stream);
 proj_status proj_quantize_weights(proj_ctx *ctx, const void *W, int64_t N, int64_t K, int group, uint32_t *codes,

@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import dense_linear_projection_amd as dlp
 from tests import decode_reference as ref
 from tests.test_gpu_quant import BF16, F32, make, run
 
@@ -69,3 +70,18 @@ def test_epilogue_of_infinities(ctx, M):
     for out in (F32, BF16):
         got = run(ctx, X, codes, scales, z, 64, b, 1, out)[:1]
         ref.close(got, want, torch.zeros_like(want))
+
+
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("sdt", [BF16, F32])
+@pytest.mark.parametrize("odd", [math.nan, math.inf, -math.inf])
+def test_quantize_keeps_what_is_not_finite_visible(ctx, zeros, sdt, odd):
+    """A group with such a weight is NaN as a whole; the others are as without it."""
+    g = torch.Generator().manual_seed(31)
+    W = torch.randn(6, 136, generator=g).to(BF16)
+    before = [t if t is None else t.cpu() for t in dlp.proj_quantize_weights(ctx, W.cuda(), 64, zeros, sdt)]
+    W[1, 3], W[4, 64 + 63], W[5, 135] = odd, odd, odd          # the last in a short group
+    after = [t if t is None else t.cpu() for t in dlp.proj_quantize_weights(ctx, W.cuda(), 64, zeros, sdt)]
+    want, got = ref.weights(*before, 64), ref.weights(*after, 64)
+    want[1, :64] = want[4, 64:128] = want[5, 128:] = math.nan
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[~torch.isnan(want)], want[~torch.isnan(want)])
