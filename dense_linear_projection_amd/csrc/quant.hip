@@ -747,7 +747,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_
             lo = fminf(lo, __shfl_xor(lo, h, 64));
             hi = fmaxf(hi, __shfl_xor(hi, h, 64));
         }
-        float s = zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+        const float range = hi - lo;  // past the largest float for weights at both its ends
+        float s = !zeros ? fmaxf(hi, -lo) / 7.f : range <= kLargest ? range / 15.f : hi / 15.f - lo / 15.f;
         if (!scales_f32) s = bf16_bits_to_f32(f32_to_bf16_bits(s));
         if (__any(!finite)) s = __builtin_nanf("");  // the extremes above leave a NaN out
         const float z = !zeros ? 8.f : s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;

@@ -85,3 +85,15 @@ def test_quantize_keeps_what_is_not_finite_visible(ctx, zeros, sdt, odd):
     want, got = ref.weights(*before, 64), ref.weights(*after, 64)
     want[1, :64] = want[4, 64:128] = want[5, 128:] = math.nan
     assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[~torch.isnan(want)], want[~torch.isnan(want)])
+
+
+@pytest.mark.parametrize("sdt", [BF16, F32])
+def test_quantize_weights_at_both_ends(ctx, sdt):
+    """A range of twice the largest float: every weight within half a scale, and what the scale's rounding moves."""
+    g = torch.Generator().manual_seed(32)
+    W = (torch.rand(3, 64, generator=g) * 6.6e38 - 3.3e38).to(BF16)
+    W[:, 0], W[:, 1] = 3.3e38, -3.3e38
+    codes, scales, z = dlp.proj_quantize_weights(ctx, W.cuda(), 64, True, sdt)
+    assert torch.isfinite(scales).all()
+    got, s = ref.weights(codes.cpu(), scales.cpu(), z.cpu(), 64), scales.cpu().double()
+    assert float(((got - W.double()).abs() / s).max()) <= 1.0 + 16 * ref.HALF[sdt]
