@@ -91,7 +91,7 @@ def test_quantize_keeps_what_is_not_finite_visible(ctx, zeros, sdt, odd):
 def test_quantize_weights_at_both_ends(ctx, sdt):
     """A range of twice the largest float: every weight within half a scale, and what the scale's rounding moves."""
     g = torch.Generator().manual_seed(32)
-    W = (torch.rand(3, 64, generator=g) * 6.6e38 - 3.3e38).to(BF16)
+    W = (torch.rand(3, 64, generator=g).double() * 6.6e38 - 3.3e38).to(BF16)
     W[:, 0], W[:, 1] = 3.3e38, -3.3e38
     codes, scales, z = dlp.proj_quantize_weights(ctx, W.cuda(), 64, True, sdt)
     assert torch.isfinite(scales).all()
