@@ -446,6 +446,18 @@ def _dtypes():
     return _types
 
 
+def _new(shapes_and_types, device, stream):
+    """Tensors in the memory of `stream` (default: torch's current stream),
+    which the allocator hands on only behind that stream's work."""
+    import torch
+    if stream is None:
+        return [torch.empty(s, dtype=t, device=device) for s, t in shapes_and_types]
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return [torch.empty(s, dtype=t, device=device) for s, t in shapes_and_types]
+
+
 def proj_pack_codes(ctx, q, codes=None, stream=None):
     """Lay out 4-bit codes given one to a byte (uint8 [N, K], K a multiple of
     8) as int32 words [N, K / 8] (allocated here if not given): of eight
@@ -456,7 +468,7 @@ def proj_pack_codes(ctx, q, codes=None, stream=None):
         raise ValueError("q must be uint8 [N, K] with K a multiple of 8")
     N, K = q.shape
     if codes is None:
-        codes = torch.empty((N, K // 8), dtype=torch.int32, device=q.device)
+        codes, = _new([((N, K // 8), torch.int32)], q.device, stream)
     _is_tensor("codes", codes, (torch.int32,), (N, K // 8))
     _check(lib().proj_pack_codes(ctx, _ptr(q), N, K, _ptr(codes), _stream(stream)), ctx)
     return codes
@@ -475,9 +487,9 @@ def proj_quantize_weights(ctx, W, group=128, zeros=True, scale_dtype=None, strea
         raise ValueError("scale_dtype must be bfloat16 or float32")
     N, K = W.shape
     G = -(-K // group)
-    codes = torch.empty((N, K // 8), dtype=torch.int32, device=W.device)
-    scales = torch.empty((N, G), dtype=dt, device=W.device)
-    z = torch.empty((N, G), dtype=torch.uint8, device=W.device) if zeros else None
+    codes, scales, z = _new([((N, K // 8), torch.int32), ((N, G), dt), ((N, G if zeros else 0), torch.uint8)], W.device, stream)
+    if not zeros:
+        z = None
     _check(lib().proj_quantize_weights(ctx, _ptr(W), N, K, int(group), _ptr(codes), _ptr(scales),
                                        OUT_F32 if dt == torch.float32 else OUT_BF16, _ptr(z), _stream(stream)), ctx)
     return codes, scales, z

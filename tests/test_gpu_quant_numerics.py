@@ -97,3 +97,29 @@ def test_quantize_weights_at_both_ends(ctx, sdt):
     assert torch.isfinite(scales).all()
     got, s = ref.weights(codes.cpu(), scales.cpu(), z.cpu(), 64), scales.cpu().double()
     assert float(((got - W.double()).abs() / s).max()) <= 1.0 + 16 * ref.HALF[sdt]
+
+
+def stream_of(t):
+    """The stream that the allocator keeps a tensor's memory for."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_registered_weights_belong_to_their_stream(ctx, as_handle):
+    """Made on a stream, codes and scales are in its memory: freed, they go to
+    later work of that stream, not to another that does not wait for it."""
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if as_handle else s
+    W = torch.randn(640, 1024, device="cuda").to(BF16)
+    q = torch.randint(0, 16, (640, 1024), device="cuda", dtype=torch.uint8)
+    s.wait_stream(torch.cuda.current_stream())
+    made = [t for t in dlp.proj_quantize_weights(ctx, W, 32, stream=stream)] + [dlp.proj_pack_codes(ctx, q, stream=stream)]
+    assert [stream_of(t) for t in made] == [s.cuda_stream] * 4
+    assert [stream_of(t) for t in dlp.proj_quantize_weights(ctx, W, 32)] == [torch.cuda.current_stream().cuda_stream] * 3
+    with torch.cuda.stream(s):
+        assert [stream_of(t) for t in dlp.proj_quantize_weights(ctx, W, 32, stream=0)] == [0] * 3
+    s.synchronize()
+    for a, b in zip(made, dlp.proj_quantize_weights(ctx, W, 32) + (dlp.proj_pack_codes(ctx, q),)):
+        assert torch.equal(a, b)
