@@ -500,7 +500,9 @@ def proj_run_quant(ctx, X, codes, scales, zeros, group, bias, epilogue, Y, strea
     scales[n, k // group] * (code[n, k] - zeros[n, k // group]) (zeros None:
     8).  X bf16 [M, K], codes int32 [N, K / 8], scales bf16 or float32 and
     zeros uint8 [N, ceil(K / group)], bias bf16 [N] or None, Y float32 /
-    bfloat16 [M, N]; all contiguous device tensors."""
+    bfloat16 [M, N]; all contiguous device tensors.  X should start at a
+    16-byte boundary: one that does not is right, but about 90 times slower
+    with many rows."""
     T = _types or _dtypes()
     _is_tensor("X", X, T.bf16)
     _is_tensor("codes", codes, T.i32)
@@ -563,7 +565,8 @@ def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=
     `positions` (int32 [T]) of rope float32 [positions, rot] (cosines, then
     sines); queries go to q_out bf16 [T, q_heads, head_dim] (None: dropped),
     keys and values into the cache's slots (int64 [T], page * page_size +
-    place; negative: a padding token, not stored)."""
+    place; negative: a padding token, not stored; two tokens with one slot: a
+    mix of both)."""
     D = _types or _dtypes()
     _is_tensor("qkv", qkv, D.bf16)
     if qkv.dim() != 2:

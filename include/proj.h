@@ -41,7 +41,8 @@
  * recorded into a HIP graph (stream capture) -- see "Capture" below.
  *
  * Memory the library owns: per context, the split-K workspace (exactly the
- * caller's bound, given to proj_create) and 1.25 KiB of zero page and sink;
+ * caller's bound, given to proj_create), 1.25 KiB of zero page and sink and
+ * 64 KiB of counters (proj_kv_attend);
  * per tuning call, the flush buffer and operand copies above; per GPU, the 2 MiB static array
  * of split-K partials that proj_run_noalloc uses (part of the library's code
  * object, held until the process ends).  Nothing else.
@@ -59,9 +60,9 @@
  * do not fit the context's workspace, are skipped).  PROJ_LOG=1 prints each
  * plan decision (tuned, default, loaded) to stderr.
  *
- * Threading: a context holds one split-K partial workspace.  Calls that may
- * run at the same time on the GPU (different streams) must use different
- * contexts, or the caller must order them.  Host-side, a context may be used from one
+ * Threading: a context holds one split-K partial workspace and one set of
+ * counters.  Calls that may run at the same time on the GPU (different streams)
+ * must use different contexts, or the caller must order them.  Host-side, a context may be used from one
  * thread at a time.
  */
 #ifndef PROJ_H
@@ -293,8 +294,11 @@ proj_status proj_quantize_weights(proj_ctx *ctx, const void *W, int64_t N, int64
  * applied: such outputs are worked out one by one, 50 ms for 1024 x 8192 of them
  * at K = 8192.  Allocates nothing and never synchronises, so it may be captured;
  * which kernel runs follows from sizes and alignment alone (no tuning, no
- * plan), so the same call gives the same bits every time.  Codes that are not
- * 4-byte aligned, scales or X not aligned to their type: PROJ_ERR_INVALID_ARG. */
+ * plan), so the same call gives the same bits every time.  An X that does not
+ * start at a 16-byte boundary is right but slow: its kernel does not use the
+ * matrix cores (12.8 ms instead of 0.14 for M = 1024, K = N = 8192).  Codes that
+ * are not 4-byte aligned, scales or X not aligned to their type:
+ * PROJ_ERR_INVALID_ARG. */
 proj_status proj_run_quant(proj_ctx *ctx, const void *X, const uint32_t *codes, const void *scales, int scale_dtype,
                            const uint8_t *zeros, int group, const void *bias, int epilogue, int64_t M, int64_t N,
                            int64_t K, void *Y, int out_dtype, void *stream);
@@ -337,8 +341,10 @@ typedef struct {
  * clamped to +-448 first (NaN stays).  A negative slot marks a padding token,
  * which is not stored.  A slot past the cache is not stored either.  A
  * position outside the table makes that token's q_out row NaN and stores
- * nothing.  Two tokens with one slot: either may remain.  Allocates nothing
- * and never synchronises. */
+ * nothing.  Two tokens with one slot: every element is one of theirs, but not
+ * all need be of the same token, and which they are may differ from call to
+ * call.  qkv and q_out are 16-byte aligned and qkv_stride a multiple of 8
+ * (PROJ_ERR_INVALID_ARG otherwise).  Allocates nothing and never synchronises. */
 proj_status proj_kv_append(proj_ctx *ctx, const proj_kv_cache *cache, const void *qkv, int64_t qkv_stride, int64_t T,
                            int q_heads, const float *rope, int64_t rope_rows, int rot, int interleaved,
                            const int32_t *positions, const int64_t *slots, void *q_out, void *stream);
@@ -349,12 +355,14 @@ proj_status proj_kv_append(proj_ctx *ctx, const proj_kv_cache *cache, const void
  *     lse = log sum_t exp(w[t]),
  * over t in [max(0, n - window), n) (window 0: all) with n = lengths[b].
  * Token t is in page tables[b * table_stride + t / page_size].  n = 0 (a
- * padding place): out = 0, lse = -infinity.  What lies outside that range, in
+ * padding place), or no w[t] above -infinity: out = 0, lse = -infinity.  What lies outside that range, in
  * the table or the cache, is not used, NaN included.  n above max_len, n < 0,
  * or a page of the range outside the cache: that sequence's out and lse are
  * NaN and nothing outside the cache is read.  max_len (at most table_width *
- * page_size) bounds the lengths and shapes the launch.  q bf16: row b at
- * q + b * q_stride, heads contiguous; out fp32 or bf16 [B][q_heads][head_dim];
+ * page_size) bounds the lengths and shapes the launch: the parts of the length
+ * are cut for sequences that long, so one far above the lengths leaves short
+ * sequences few and long parts.  q bf16: row b at q + b * q_stride, heads
+ * contiguous, 16-byte aligned, q_stride a multiple of 8; out (16-byte aligned) fp32 or bf16 [B][q_heads][head_dim];
  * lse fp32 [B][q_heads] or NULL.  Sums and softmax are fp32;
  * a probability meets the values with all of its 24 bits for fp32 results, rounded
  * to 16 for bf16 ones.  The split over the length follows from B, heads, max_len, window and the context's workspace,

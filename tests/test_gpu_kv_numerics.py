@@ -102,3 +102,22 @@ def test_large_negative_scale(ctx):
     o, e = run_attend(ctx, cache, q, tables, n, -1.5, F32)
     ref.close(o, want[0], tol[0])
     ref.close(e, want[1], tol[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("rot", [64, 34])
+def test_tokens_of_one_slot(ctx, dtype, rot):
+    """Every element of a slot that several tokens go to is one of theirs; other slots keep what they had."""
+    T, H, D = 300, 2, 64
+    g = torch.Generator().manual_seed(27)
+    qkv = torch.randn(T, 2 * H * D, generator=g).to(BF16)
+    cache = dlp.kv_cache(*(torch.zeros(2, H, 16, D, device="cuda").to(dtype) for _ in range(2)))
+    rope = torch.cat((torch.ones(1, rot // 2), torch.zeros(1, rot // 2)), 1).cuda()
+    dlp.proj_kv_append(ctx, cache, qkv.cuda(), rope, torch.zeros(T, dtype=torch.int32, device="cuda"),
+                       torch.full((T,), 21, device="cuda"))
+    x = qkv.to(dtype).float().view(T, 2, H, D)
+    for i, c in enumerate((cache.k, cache.v)):
+        c = c.float().cpu()
+        assert bool((c[1, :, 5] == x[:, i]).any(0).all())
+        c[1, :, 5] = 0
+        assert not c.any()
