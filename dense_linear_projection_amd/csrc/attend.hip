@@ -22,15 +22,14 @@
 //     4 g + i (i < 4) or 16 + 4 g + i - 4; V follows by being read in that
 //     order with LDS's transposing loads.  So the probabilities never leave
 //     the registers.
-//   * a probability enters as bf16 terms of 8 bits each: for fp32 results three,
-//     which together are its 24 bits; for bf16 results two (48 sequences with a
-//     window: 17.3 us with two, 21.9 with three; two leave fp32 results 4e-6 off
-//     where three leave 3e-7).  All but the last are cut, so that what is left is
-//     never negative; the last is rounded to nearest, so that with two a
-//     probability is off by 2^-17 at most and either way (cut, all were low and
-//     results with them, by 6e-6).  Those after the first are at least 2^-30 of it,
-//     so that an infinite value does not meet a zero, and zero where it is, so
-//     that a vanished probability takes nothing from a large value.
+//   * a probability enters as three bf16 terms of 8 bits each, which together
+//     are its 24 bits.  Two would be faster by 1% (6% with 8-bit keys: 64
+//     sequences of 2000 tokens 40.6 us, with three 43), but four of a thousand
+//     bf16 results were then not the correctly rounded ones, where fp32 sums
+//     leave half of one.  The terms are cut, so that what is left is never
+//     negative; those after the first are at least 2^-30 of it, so that an
+//     infinite value does not meet a zero, and zero where it is, so that a
+//     vanished probability takes nothing from a large value.
 //   * K and V are read a KB at a time (whole rows, in the order they lie) into
 //     registers, put into LDS and read from there as the products need them;
 //     those of the next tile are on their way while this one is computed, 16 KB
@@ -54,6 +53,7 @@ typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4;
 typedef __attribute__((__vector_size__(2 * sizeof(int)))) int i32x2;
 typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 
+constexpr int kTerms = 3;          // bf16 terms of a probability
 constexpr int kChunk = 2048;       // tokens whose pages are staged at once
 constexpr int kJoined = 32;         // parts that the attention kernel joins itself (500 tokens: 8.0 us, in two kernels 9.3)
 constexpr float kLowest = -0x1.fffffep127f;  // a running maximum before the first logit: the lowest finite one
@@ -140,7 +140,7 @@ __device__ __forceinline__ float2 get_part(const float *from) {
 }
 
 // Two workgroups to a compute unit where their registers (and 160 KB of LDS) allow it.
-template <int D, bool FP8, int QT, bool ONCE, int TERMS>
+template <int D, bool FP8, int QT, bool ONCE>
 __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(AttendArgs a) {
     using C = AttendCfg<D, FP8, QT>;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                     for (int t = 0; t < QT; ++t) s[t][x] = mfma16x16x32(k, q[t][i], s[t][x]);
                 }
 
-            bf16x8 prob[QT][TERMS];
+            bf16x8 prob[QT][kTerms];
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
                 float w[8], most = kLowest;
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
 #pragma unroll
                     for (int i = 0; i < C::DT; ++i) o[t][i] *= f;
                 }
-                uint32_t bits[TERMS][4];
+                uint32_t bits[kTerms][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float p[2], least[2];
@@ -310,16 +310,15 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                         least[e] = p[e] * 0x1p-30f;
                     }
 #pragma unroll
-                    for (int k = 0; k < TERMS - 1; ++k) {
+                    for (int k = 0; k < kTerms; ++k) {
                         const uint32_t u0 = __float_as_uint(p[0]) & 0xffff0000u, u1 = __float_as_uint(p[1]) & 0xffff0000u;
                         bits[k][i] = (u0 >> 16) | u1;
                         p[0] = fmaxf(p[0] - __uint_as_float(u0), least[0]);
                         p[1] = fmaxf(p[1] - __uint_as_float(u1), least[1]);
                     }
-                    bits[TERMS - 1][i] = f32_to_bf16_bits(p[0]) | static_cast<uint32_t>(f32_to_bf16_bits(p[1])) << 16;
                 }
 #pragma unroll
-                for (int k = 0; k < TERMS; ++k)
+                for (int k = 0; k < kTerms; ++k)
                     prob[t][k] = __builtin_bit_cast(bf16x8, u32x4{bits[k][0], bits[k][1], bits[k][2], bits[k][3]});
             }
 
@@ -355,7 +354,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
 #pragma unroll
                 for (int t = 0; t < QT; ++t)
 #pragma unroll
-                    for (int k = 0; k < TERMS; ++k) o[t][i] = mfma16x16x32(v, prob[t][k], o[t][i]);
+                    for (int k = 0; k < kTerms; ++k) o[t][i] = mfma16x16x32(v, prob[t][k], o[t][i]);
             }
             asm volatile("" ::: "memory");
             __builtin_amdgcn_wave_barrier();
@@ -489,14 +488,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
 }
 
 // Instantiated here: the launchers below are compiled for the host only.
-#define PROJ_ATTEND_AS(D, QT, ONCE, TERMS)                                           \
-    template __global__ void attend_kernel<D, false, QT, ONCE, TERMS>(AttendArgs);  \
-    template __global__ void attend_kernel<D, true, QT, ONCE, TERMS>(AttendArgs);
-#define PROJ_ATTEND_QT(D, QT)         \
-    PROJ_ATTEND_AS(D, QT, false, 2)   \
-    PROJ_ATTEND_AS(D, QT, false, 3)   \
-    PROJ_ATTEND_AS(D, QT, true, 2)    \
-    PROJ_ATTEND_AS(D, QT, true, 3)
+#define PROJ_ATTEND_QT(D, QT)                                              \
+    template __global__ void attend_kernel<D, false, QT, false>(AttendArgs); \
+    template __global__ void attend_kernel<D, true, QT, false>(AttendArgs);  \
+    template __global__ void attend_kernel<D, false, QT, true>(AttendArgs);  \
+    template __global__ void attend_kernel<D, true, QT, true>(AttendArgs);
 #define PROJ_ATTEND_INST(D) \
     PROJ_ATTEND_QT(D, 1)    \
     template __global__ void attend_join_kernel<D>(AttendArgs);
@@ -568,17 +564,14 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
                                  (reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v)) % 128 == 0);
     a.by_die = mixed && a.B * parts >= 8;
     const int64_t grid = a.by_die ? (a.B * parts + 7) / 8 * 8 * hh : rows * parts;
-    auto pick = [&](auto two, auto terms) {
-        constexpr int QT = decltype(two)::value, TERMS = decltype(terms)::value;
-        if (a.c.fp8) return once ? attend_kernel<D, true, QT, true, TERMS> : attend_kernel<D, true, QT, false, TERMS>;
-        return once ? attend_kernel<D, false, QT, true, TERMS> : attend_kernel<D, false, QT, false, TERMS>;
+    auto pick = [&](auto two) {
+        constexpr int QT = decltype(two)::value;
+        if (a.c.fp8) return once ? attend_kernel<D, true, QT, true> : attend_kernel<D, true, QT, false>;
+        return once ? attend_kernel<D, false, QT, true> : attend_kernel<D, false, QT, false>;
     };
-    auto pick_terms = [&](auto two) {
-        return a.out_dtype == OUT_F32 ? pick(two, std::integral_constant<int, 3>()) : pick(two, std::integral_constant<int, 2>());
-    };
-    auto kernel = pick_terms(std::integral_constant<int, 1>());
+    auto kernel = pick(std::integral_constant<int, 1>());
     if constexpr (kTwo)
-        if (qt == 2) kernel = pick_terms(std::integral_constant<int, 2>());
+        if (qt == 2) kernel = pick(std::integral_constant<int, 2>());
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || parts == 1 || a.join) return e;

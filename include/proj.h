@@ -363,9 +363,9 @@ proj_status proj_kv_append(proj_ctx *ctx, const proj_kv_cache *cache, const void
  * are cut for sequences that long, so one far above the lengths leaves short
  * sequences few and long parts.  q bf16: row b at q + b * q_stride, heads
  * contiguous, 16-byte aligned, q_stride a multiple of 8; out (16-byte aligned) fp32 or bf16 [B][q_heads][head_dim];
- * lse fp32 [B][q_heads] or NULL.  Sums and softmax are fp32;
- * a probability meets the values with all of its 24 bits for fp32 results, rounded
- * to 16 for bf16 ones.  The split over the length follows from B, heads, max_len, window and the context's workspace,
+ * lse fp32 [B][q_heads] or NULL.  Sums and softmax are fp32,
+ * and a probability meets the values with all of its 24 bits: bf16 results are
+ * the fp32 ones, rounded.  The split over the length follows from B, heads, max_len, window and the context's workspace,
  * which holds the parts' fp32 results (with none, nothing is split): the same
  * call gives the same bits every time.  Allocates nothing and never
  * synchronises. */

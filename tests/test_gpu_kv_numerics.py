@@ -16,10 +16,10 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("dtype", [BF16, FP8])
 def test_probabilities_are_not_cut_one_way(ctx, dtype):
-    """bf16 results take probabilities of 16 bits.  Rounded to nearest they are
-    off by at most 2^-17 in either direction, which cancels over results that
-    are means of about 300 tokens each; cut, each is low by about 2^-17, and so
-    is every result.  Measured against the correctly rounded results, so that
+    """Probabilities that met the values with 16 bits would be off by at most
+    2^-17: rounded to nearest in either direction, which cancels over results
+    that are means of about 300 tokens each, cut each low by about 2^-17, and
+    so every result.  Measured against the correctly rounded results, so that
     only those that fall on the other side of a rounding border differ."""
     k, v, cache, q, tables, n, scales = make_attend(32, 64, 8, 128, 16, dtype, "hnd", [280 + b for b in range(32)], 21,
                                                     poison=False)
@@ -31,6 +31,17 @@ def test_probabilities_are_not_cut_one_way(ctx, dtype):
     w = want[0]
     low = float(((o.cpu().double() - w.to(BF16).double()) / w).mean())
     assert abs(low) < 2.0 ** -18, low
+
+
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("per,lengths", [(4, [1, 500, 37, 0, 64]), (20, [900, 33]), (8, [7000])])
+def test_bf16_results_are_the_fp32_ones_rounded(ctx, D, dtype, per, lengths):
+    """Probabilities keep their 24 bits whatever the results' type: nothing but the last rounding differs."""
+    k, v, cache, q, tables, n, scales = make_attend(len(lengths), 2 * per, 2, D, 16, dtype, "hnd", lengths, 28)
+    wide, _ = run_attend(ctx, cache, q, tables, n, D ** -0.5, F32)
+    o, _ = run_attend(ctx, cache, q, tables, n, D ** -0.5, BF16)
+    assert torch.equal(o, wide.to(BF16))
 
 
 def one_head(ctx, K, V, q, n, scale, out):
@@ -52,8 +63,6 @@ def test_small_probability_of_a_large_value(ctx, out, low):
     q[0], K[1, 0], V[1] = 1, low, 3e38
     want, tol = ref.attend(K.view(1, 1, 16, 64), V.view(1, 1, 16, 64), q.view(1, 1, 64), torch.zeros(1, 1, dtype=torch.int32),
                            torch.tensor([3]), 1.0, 0, (1.0, 1.0), out)
-    if out == BF16:
-        tol[0][...] += 2.0 ** -17 * want[0].abs()      # a probability of 16 bits
     o, e = one_head(ctx, K, V, q, 3, 1.0, out)
     ref.close(o[None], want[0], tol[0])
     ref.close(e[None], want[1], tol[1])
