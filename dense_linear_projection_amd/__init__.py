@@ -501,7 +501,7 @@ def proj_run_quant(ctx, X, codes, scales, zeros, group, bias, epilogue, Y, strea
     8).  X bf16 [M, K], codes int32 [N, K / 8], scales bf16 or float32 and
     zeros uint8 [N, ceil(K / group)], bias bf16 [N] or None, Y float32 /
     bfloat16 [M, N]; all contiguous device tensors.  X should start at a
-    16-byte boundary: one that does not is right, but about 90 times slower
+    16-byte boundary: one that does not is right, but about 100 times slower
     with many rows."""
     T = _types or _dtypes()
     _is_tensor("X", X, T.bf16)

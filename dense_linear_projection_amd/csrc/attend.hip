@@ -6,9 +6,8 @@
 //     w[t][h] = scale <q[h], k[t]>,  m = max_t w,  l = sum_t exp(w - m),
 //     o[h][:] = sum_t exp(w[t][h] - m) v[t][:],
 // and parts with (m, l, o) join as (M = max m, sum exp(m - M) l, ...): one
-// pass over keys and values, which bound the call (each is read once for
-// `per` query heads: about per operations a byte, far below the matrix
-// cores' rate).
+// pass over keys and values, which bound the call (each serves `per` query
+// heads: about per operations a byte, far below the matrix cores' rate).
 //
 // A workgroup is four waves on one (sequence, key-value head, part); wave w
 // takes tiles w, w + 4, ... of 32 tokens, with its own running maximum, sum
@@ -34,11 +33,13 @@
 //     registers, put into LDS and read from there as the products need them;
 //     those of the next tile are on their way while this one is computed, 16 KB
 //     a wave at 128 elements in bf16, and nothing waits for anything but its own
-//     operands.  They are read once, and kept out of the caches
-//     (non-temporal loads, ONCE) unless heads share memory lines.
+//     operands.  They are kept out of the caches (non-temporal loads, ONCE)
+//     unless heads share memory lines: a workgroup reads them once, for 16
+//     query heads (32 where D <= 128); those of more are other workgroups, which
+//     read them again.
 // Bound by bytes where lengths are large: one sequence of 131072 tokens (8
-// heads of 128 in bf16, 537 MB) 90 us, 6.0 TB/s; 32 sequences up to 16384 tokens
-// 204 us, 5.6 TB/s; by latency where they are small: 500 tokens 8.4 us.
+// heads of 128 in bf16, 537 MB) 91 us, 6.0 TB/s; 32 sequences up to 16384 tokens
+// 205 us, 5.6 TB/s; by latency where they are small: 500 tokens 8.5 us.
 // The running maximum moves only when a logit passes it by more than 5 (a
 // factor of 148): sums stay in range, and most tiles need no rescaling and no
 // exchange between lanes.  Logits are kept in natural units, and scaled to base

@@ -56,6 +56,8 @@ __device__ __forceinline__ float quant_by_definition(int64_t m, int64_t n, int64
 // Any K (a multiple of 8), alignment and number of outputs: one wave per
 // output, lane l taking words l, l + 64, ... of the row.  A word lies within
 // one group.  A launch that cannot have a wave for every output goes round.
+// Bound by reading X two bytes at a time and the codes again for every row:
+// K = N = 8192 26 us for one row, 280 for 16, 16 ms for 1024.
 __global__ __launch_bounds__(256) void quant_rows_kernel(QuantArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t words = a.K / 8, outputs = a.M * a.N;
@@ -413,8 +415,13 @@ struct TileCfg {
 // the scales and X of s + 3; one barrier a step publishes all of it.  Loads
 // complete in order, so whatever is used a step after its issue makes all that
 // was issued before it wait: everything is used two steps after.  M = 1024,
-// K = N = 8192: 139 to 152 us, up to 990 TFLOP/s; without the memory operations the
-// loop takes 108, its matrix operations alone 98.  M = 64, N = 28672: 74 us.
+// K = N = 8192, groups of 128, no zero points: 143 us (960 TFLOP/s; 180 where the
+// clock is low); without the memory operations the loop takes 108, its matrix
+// operations alone 98.  M = 64, N = 28672, groups of 64, zero points: 73 us, with
+// vector instructions in 39% of a SIMD's cycles and matrix ones in 19%: few waves
+// (1.3 to a SIMD) that wait.  The 128 x 256 tile's registers hold what the
+// first needs; with zero points or ragged rows 2 to 104 are spilled, and each
+// reload waits for all copies (times at launch_tile).
 template <int MT, int NT, int WM, int WN, int GROUP, bool ZEROS, bool F32, int EDGE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a, int splits) {
     using C = TileCfg<MT, NT, WM, WN, GROUP>;
@@ -714,6 +721,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void quant_tile_kernel(QuantArgs a,
     }
 }
 
+// A word to a thread; bound by bytes: 8192 x 8192 20 us, 5.1 TB/s.
 __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *q, int64_t words, uint32_t *codes) {
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < words;
          i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -726,6 +734,8 @@ __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *q, int64
 
 // One wave per group of a row: the group's extremes, then its codes.  Lane l
 // holds words l of the group (16 words at most); a word is eight weights.
+// Weights are registered once: 8192 x 8192 takes 269 us with groups of 128, 519 of
+// 64, 1001 of 32, bound by the waves, of whose lanes 16, 8 or 4 hold weights.
 __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t *W, int64_t N, int64_t K, int64_t G, int group,
                                                        uint32_t *codes, void *scales, int scales_f32, uint8_t *zeros) {
     const int lane = threadIdx.x & 63;
@@ -875,7 +885,10 @@ static hipError_t run_tile(const QuantArgs &a, hipStream_t st) {
 template <int GROUP, bool ZEROS, int EDGE>
 static hipError_t launch_tile(const QuantArgs &a, hipStream_t st) {
     // large tiles once there are enough of them (K = 8192, N = 8192; us with 128 x 256
-    // and with 64 x 128 tiles): M = 256 71, 58; M = 512 107, 96; M = 1024 152, 224
+    // and with 64 x 128 tiles; groups of 128, no zero points): M = 256 71, 58;
+    // M = 512 107, 96; M = 1024 159, 196.  The rule is that combination's: M = 1024
+    // with groups of 64 175, 221, with zero points and groups of 128 170, 223, of 64
+    // 349, 252, of 32 729, 305; K = 8160 with zero points and groups of 128 280, 254
     if (((a.M + 127) / 128) * ((a.N + 255) / 256) * 2 > a.cus) return run_tile<4, 4, 2, 4, GROUP, ZEROS, EDGE>(a, st);
     return run_tile<4, 2, 1, 4, GROUP, ZEROS, EDGE>(a, st);
 }

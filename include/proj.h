@@ -296,7 +296,7 @@ proj_status proj_quantize_weights(proj_ctx *ctx, const void *W, int64_t N, int64
  * which kernel runs follows from sizes and alignment alone (no tuning, no
  * plan), so the same call gives the same bits every time.  An X that does not
  * start at a 16-byte boundary is right but slow: its kernel does not use the
- * matrix cores (12.8 ms instead of 0.14 for M = 1024, K = N = 8192).  Codes that
+ * matrix cores (16 ms instead of 0.14 for M = 1024, K = N = 8192).  Codes that
  * are not 4-byte aligned, scales or X not aligned to their type:
  * PROJ_ERR_INVALID_ARG. */
 proj_status proj_run_quant(proj_ctx *ctx, const void *X, const uint32_t *codes, const void *scales, int scale_dtype,
