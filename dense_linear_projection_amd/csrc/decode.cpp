@@ -51,7 +51,8 @@ proj_status check_cache(proj_ctx *ctx, const proj_kv_cache *c, CacheArgs *out) {
                              (int)c->heads, (long long)c->pages, (int)c->page_size);
     if (!attend_dim(c->head_dim))
         return context_error(ctx, PROJ_ERR_UNSUPPORTED, "head size %d (64, 80, 96, 128, 192 or 256)", (int)c->head_dim);
-    if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
+    // a cache without pages has no memory either
+    if ((c->pages > 0 && (!c->k || !c->v)) || !aligned(c->k, 16) || !aligned(c->v, 16))
         return context_error(ctx, PROJ_ERR_INVALID_ARG, "cache: k or v is NULL or not 16-byte aligned");
     const int64_t unit = c->dtype == PROJ_KV_FP8 ? 16 : 8;
     for (int i = 0; i < 3; ++i)

@@ -311,7 +311,7 @@ proj_status proj_run_quant(proj_ctx *ctx, const void *X, const uint32_t *codes, 
  * 256) elements.  Element d of head h, token t of page p sits at element
  * p * strides[0] + h * strides[1] + t * strides[2] + d of k (v), so pages may
  * be head-major or token-major; strides are multiples of 8 (bf16) or 16
- * (fp8) elements and k and v 16-byte aligned.  PROJ_KV_FP8 holds OCP e4m3 values: the value is the
+ * (fp8) elements and k and v 16-byte aligned (NULL where pages is 0).  PROJ_KV_FP8 holds OCP e4m3 values: the value is the
  * stored one times k_scale (v_scale); for PROJ_KV_BF16 the scales are 1. */
 typedef enum {
     PROJ_KV_BF16 = 0,

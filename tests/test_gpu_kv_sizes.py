@@ -42,3 +42,17 @@ def test_unsplit_sequences_of_many_pages(page, dtype, layout, window):
         ref.close(e, want[1], tol[1])
     finally:
         dlp.proj_destroy(small)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+def test_cache_without_pages(ctx, dtype):
+    """Nothing can be stored, and what is empty is attended: 0 and minus infinity, NaN where a token is asked for."""
+    cache = dlp.kv_cache(*(torch.empty(0, 2, 16, 64, device="cuda").to(dtype) for _ in range(2)))
+    qkv = torch.randn(3, 8 * 64, device="cuda").to(BF16)
+    q, rope = torch.empty(3, 4, 64, device="cuda", dtype=BF16), torch.zeros(1, 0, device="cuda")
+    dlp.proj_kv_append(ctx, cache, qkv, rope, torch.zeros(3, dtype=torch.int32, device="cuda"),
+                       torch.tensor([0, -1, 5], device="cuda"), q)
+    assert torch.equal(q, qkv[:, :256].view(3, 4, 64))
+    o, e = run_attend(ctx, cache, q.cpu(), torch.zeros(3, 1, dtype=torch.int32), torch.tensor([0, 1, 0], dtype=torch.int32), 1.0, F32)
+    assert not o[[0, 2]].any() and bool(torch.isneginf(e[[0, 2]]).all())
+    assert bool(torch.isnan(o[1]).all()) and bool(torch.isnan(e[1]).all())
