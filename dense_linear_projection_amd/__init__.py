@@ -21,8 +21,12 @@ weights registered in the packed tile layout ``proj_packed_bytes``,
 ``proj_read_probe``, and ``proj_run_noalloc`` (proj_run with no device
 allocation); for 4-bit weights with group scales ``proj_pack_codes``,
 ``proj_quantize_weights``, ``proj_run_quant``; and for the paged key-value
-cache between a decoding step's projections ``proj_kv_append`` and
-``proj_kv_attend`` on a cache described once by ``kv_cache``.
+cache between a decoding step's projections ``proj_kv_append`` (with norms of
+the query and key heads ``proj_kv_append_norm``) and ``proj_kv_attend`` (for a
+batch behind one prefix ``proj_kv_attend_shared``) on a cache described once by
+``kv_cache``; for 8-bit integers with a scale for each token and output
+``proj_quantize_rows``, ``proj_run_int`` and, from bf16 tokens,
+``proj_run_int_dynamic``.
 """
 from __future__ import annotations
 
@@ -51,7 +55,8 @@ EXPORTS = ["proj_create", "proj_run", "proj_tune", "proj_destroy", "proj_status_
            "proj_candidate_name_hilo", "proj_run_candidate_hilo", "proj_packed_bytes", "proj_pack_weights",
            "proj_run_packed", "proj_get_plan_packed", "proj_num_candidates_packed", "proj_candidate_name_packed",
            "proj_run_candidate_packed", "proj_read_probe", "proj_run_noalloc",
-           "proj_pack_codes", "proj_quantize_weights", "proj_run_quant", "proj_kv_append", "proj_kv_attend"]
+           "proj_pack_codes", "proj_quantize_weights", "proj_run_quant", "proj_kv_append", "proj_kv_attend",
+           "proj_quantize_rows", "proj_run_int", "proj_run_int_dynamic", "proj_kv_append_norm", "proj_kv_attend_shared"]
 
 
 class ProjError(RuntimeError):
@@ -118,6 +123,12 @@ def lib() -> ctypes.CDLL:
         "proj_run_quant": ([vp, vp, vp, vp, ci, vp, ci, vp, ci, i64, i64, i64, vp, ci, vp], st),
         "proj_kv_append": ([vp, vp, vp, i64, i64, ci, vp, i64, ci, ci, vp, vp, vp, vp], st),
         "proj_kv_attend": ([vp, vp, vp, i64, i64, ci, vp, i64, i64, vp, i64, i64, ctypes.c_float, vp, ci, vp, vp], st),
+        "proj_quantize_rows": ([vp, vp, i64, i64, i64, vp, i64, vp, vp], st),
+        "proj_run_int": ([vp, vp, vp, vp, vp, vp, ci, i64, i64, i64, vp, ci, vp], st),
+        "proj_run_int_dynamic": ([vp, vp, i64, vp, vp, vp, ci, i64, i64, i64, vp, ci, vp], st),
+        "proj_kv_append_norm": ([vp, vp, vp, i64, i64, ci, vp, vp, ci, ci, ctypes.c_float, vp, i64, ci, ci, vp, vp, vp, vp], st),
+        "proj_kv_attend_shared": ([vp, vp, vp, i64, i64, ci, vp, i64, vp, i64, i64, vp, i64, i64, ctypes.c_float, vp, ci, vp,
+                                   vp], st),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -433,7 +444,7 @@ class _Types:
         import torch
         self.f32 = torch.float32
         self.bf16, self.fp32, self.float = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
-        self.u8, self.i32, self.i64 = (torch.uint8,), (torch.int32,), (torch.int64,)
+        self.u8, self.i8, self.i32, self.i64 = (torch.uint8,), (torch.int8,), (torch.int32,), (torch.int64,)
 
 
 _types = None
@@ -523,6 +534,70 @@ def proj_run_quant(ctx, X, codes, scales, zeros, group, bias, epilogue, Y, strea
         _check(st, ctx)
 
 
+# ------------------------- 8-bit integers, a scale to each token and output
+
+def proj_quantize_rows(ctx, X, q=None, scales=None, stream=None):
+    """8-bit integers of bf16 rows X [M, K] (rows may be strided): (q int8
+    [M, K rounded up to a multiple of 16], zero behind K, scales float32 [M]),
+    allocated here unless given.  scales = max |row| / 127 and q = rint(127 x /
+    max |row|): the tokens and the weights that proj_run_int takes."""
+    T = _types or _dtypes()
+    _is_tensor("X", X, T.bf16)
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    M, K = X.shape
+    padded = -(-K // 16) * 16
+    if q is None or scales is None:
+        made = _new([((M, padded), T.i8[0]), ((M,), T.f32)], X.device, stream)
+        q, scales = made[0] if q is None else q, made[1] if scales is None else scales
+    x, stride = _rows("X", X, K)
+    _check((_lib or lib()).proj_quantize_rows(ctx, x, stride, M, K, _operand("q", q, T.i8, (M, padded)), padded,
+                                              _operand("scales", scales, T.fp32, (M,)), _stream(stream)), ctx)
+    return q, scales
+
+
+def proj_run_int(ctx, X, x_scales, W, w_scales, bias, epilogue, Y, stream=None) -> None:
+    """Enqueue Y = epilogue(x_scales[m] * w_scales[n] * sum_k X[m, k] W[n, k]
+    [+ bias]): X int8 [M, K] and W int8 [N, K], K a multiple of 16 (as
+    proj_quantize_rows pads them), x_scales and w_scales float32 [M] and [N],
+    bias bf16 [N] or None, Y float32 / bfloat16 [M, N]; all contiguous device
+    tensors, X and W starting at 16-byte boundaries."""
+    T = _types or _dtypes()
+    _is_tensor("X", X, T.i8)
+    _is_tensor("W", W, T.i8)
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X [M, K] and W [N, K] must have two dimensions")
+    M, K = X.shape
+    N = W.shape[0]
+    st = (_lib or lib()).proj_run_int(
+        ctx, _operand("X", X, T.i8, (M, K)), _operand("x_scales", x_scales, T.fp32, (M,)), _operand("W", W, T.i8, (N, K)),
+        _operand("w_scales", w_scales, T.fp32, (N,)), None if bias is None else _operand("bias", bias, T.bf16, (N,)), epilogue,
+        M, N, K, _operand("Y", Y, T.float, (M, N)), OUT_F32 if Y.dtype == T.f32 else OUT_BF16, _stream(stream))
+    if st:
+        _check(st, ctx)
+
+
+def proj_run_int_dynamic(ctx, X, W, w_scales, bias, epilogue, Y, stream=None) -> None:
+    """proj_run_int from bf16 tokens X [M, K] (rows may be strided), made
+    integers row by row in the context's workspace; W int8 [N, K rounded up to a
+    multiple of 16], zero behind K.  Tokens that meet several projections are
+    made integers once with proj_quantize_rows instead."""
+    T = _types or _dtypes()
+    _is_tensor("X", X, T.bf16)
+    _is_tensor("W", W, T.i8)
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X [M, K] and W [N, K] must have two dimensions")
+    M, K = X.shape
+    N = W.shape[0]
+    x, stride = _rows("X", X, K)
+    st = (_lib or lib()).proj_run_int_dynamic(
+        ctx, x, stride, _operand("W", W, T.i8, (N, -(-K // 16) * 16)), _operand("w_scales", w_scales, T.fp32, (N,)),
+        None if bias is None else _operand("bias", bias, T.bf16, (N,)), epilogue, M, N, K, _operand("Y", Y, T.float, (M, N)),
+        OUT_F32 if Y.dtype == T.f32 else OUT_BF16, _stream(stream))
+    if st:
+        _check(st, ctx)
+
+
 # ------------------------------------------------- paged key-value cache
 
 class kv_cache:
@@ -558,16 +633,8 @@ def _rows(name, t, width):
     return t.data_ptr(), width if t.shape[0] == 1 else t.stride(0)
 
 
-def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=None, interleaved=False,
-                   stream=None) -> None:
-    """Enqueue one append: of qkv bf16 [T, (q_heads + 2 * heads) * head_dim]
-    (rows may be strided) the query and key heads are rotated by the rows
-    `positions` (int32 [T]) of rope float32 [positions, rot] (cosines, then
-    sines); queries go to q_out bf16 [T, q_heads, head_dim] (None: dropped),
-    keys and values into the cache's slots (int64 [T], page * page_size +
-    place; negative: a padding token, not stored; two tokens with one slot: a
-    mix of both)."""
-    D = _types or _dtypes()
+def _append_shape(cache, qkv, rope, q_heads, D):
+    """(tokens, query heads, pointer and row stride of qkv)"""
     _is_tensor("qkv", qkv, D.bf16)
     if qkv.dim() != 2:
         raise ValueError("qkv must be [T, width]")
@@ -579,10 +646,45 @@ def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=
     _is_tensor("rope", rope, D.fp32)
     if rope.dim() != 2:
         raise ValueError("rope must be [positions, rot]")
-    x, stride = _rows("qkv", qkv, width)
+    return (T, heads) + _rows("qkv", qkv, width)
+
+
+def proj_kv_append(ctx, cache, qkv, rope, positions, slots, q_out=None, q_heads=None, interleaved=False,
+                   stream=None) -> None:
+    """Enqueue one append: of qkv bf16 [T, (q_heads + 2 * heads) * head_dim]
+    (rows may be strided) the query and key heads are rotated by the rows
+    `positions` (int32 [T]) of rope float32 [positions, rot] (cosines, then
+    sines); queries go to q_out bf16 [T, q_heads, head_dim] (None: dropped),
+    keys and values into the cache's slots (int64 [T], page * page_size +
+    place; negative: a padding token, not stored; two tokens with one slot: a
+    mix of both)."""
+    D = _types or _dtypes()
+    T, heads, x, stride = _append_shape(cache, qkv, rope, q_heads, D)
     st = (_lib or lib()).proj_kv_append(
         ctx, cache._p, x, stride, T, heads, _ptr(rope), rope.shape[0], rope.shape[1], 1 if interleaved else 0,
         _operand("positions", positions, D.i32, (T,)), _operand("slots", slots, D.i64, (T,)),
+        None if q_out is None else _operand("q_out", q_out, D.bf16, (T, heads, cache.head_dim)), _stream(stream))
+    if st:
+        _check(st, ctx)
+
+
+def proj_kv_append_norm(ctx, cache, qkv, q_norm, k_norm, eps, rope, positions, slots, q_out=None, q_heads=None,
+                        interleaved=False, stream=None) -> None:
+    """proj_kv_append whose query and key heads are first divided by their root
+    mean square: x / sqrt(mean(x^2) + eps) * w, with w = q_norm and k_norm
+    (bfloat16 or float32, both of one type, [head_dim] or both of each head's own
+    [q_heads, head_dim] and [heads, head_dim]; None: not normed)."""
+    D = _types or _dtypes()
+    T, heads, x, stride = _append_shape(cache, qkv, rope, q_heads, D)
+    given = [(n, t, h) for n, t, h in (("q_norm", q_norm, heads), ("k_norm", k_norm, cache.heads)) if t is not None]
+    per_head = bool(given) and given[0][1].dim() == 2
+    f32 = bool(given) and given[0][1].dtype == D.f32
+    for name, t, h in given:
+        _operand(name, t, D.fp32 if f32 else D.bf16, (h, cache.head_dim) if per_head else (cache.head_dim,))
+    st = (_lib or lib()).proj_kv_append_norm(
+        ctx, cache._p, x, stride, T, heads, _ptr(q_norm), _ptr(k_norm), OUT_F32 if f32 else OUT_BF16, 1 if per_head else 0, eps,
+        _ptr(rope), rope.shape[0], rope.shape[1], 1 if interleaved else 0, _operand("positions", positions, D.i32, (T,)),
+        _operand("slots", slots, D.i64, (T,)),
         None if q_out is None else _operand("q_out", q_out, D.bf16, (T, heads, cache.head_dim)), _stream(stream))
     if st:
         _check(st, ctx)
@@ -611,6 +713,36 @@ def proj_kv_attend(ctx, cache, q, tables, lengths, scale, out, lse=None, window=
         ctx, cache._p, qp, stride, B, heads, tp, tstride, tw, _operand("lengths", lengths, T.i32, (B,)),
         tw * cache.page_size if max_len is None else max_len, window, scale, _operand("out", out, T.float, (B, heads, D)),
         OUT_F32 if out.dtype == T.f32 else OUT_BF16,
+        None if lse is None else _operand("lse", lse, T.fp32, (B, heads)), _stream(stream))
+    if st:
+        _check(st, ctx)
+
+
+def proj_kv_attend_shared(ctx, cache, q, prefix, prefix_len, tables, lengths, scale, out, lse=None, window=0, max_len=None,
+                          stream=None) -> None:
+    """proj_kv_attend for a batch whose sequences begin with the same prefix_len
+    tokens, in the pages `prefix` (int32 [pages]); `tables` int32 [B, width] (rows
+    may be strided) hold the pages of each sequence's own tokens, while lengths,
+    window and max_len (default: the prefix and what the tables hold) count all of
+    a sequence's tokens."""
+    T = _types or _dtypes()
+    _is_tensor("q", q, T.bf16)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [B, q_heads, %d]" % cache.head_dim)
+    B, heads, D = q.shape
+    _is_tensor("tables", tables, T.i32)
+    if tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError("tables must be [B, width]")
+    _is_tensor("prefix", prefix, T.i32)
+    if prefix.dim() != 1 or prefix_len < 0 or prefix.shape[0] * cache.page_size < prefix_len:
+        raise ValueError("prefix must hold the pages of %d tokens" % prefix_len)
+    tw = tables.shape[1]
+    qp, stride = _rows("q", q, heads * D)
+    tp, tstride = _rows("tables", tables, tw)
+    st = (_lib or lib()).proj_kv_attend_shared(
+        ctx, cache._p, qp, stride, B, heads, _operand("prefix", prefix, T.i32, prefix.shape), prefix_len, tp, tstride, tw,
+        _operand("lengths", lengths, T.i32, (B,)), prefix_len + tw * cache.page_size if max_len is None else max_len, window,
+        scale, _operand("out", out, T.float, (B, heads, D)), OUT_F32 if out.dtype == T.f32 else OUT_BF16,
         None if lse is None else _operand("lse", lse, T.fp32, (B, heads)), _stream(stream))
     if st:
         _check(st, ctx)

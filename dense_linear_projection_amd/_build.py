@@ -19,7 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libproj.so")
 SOURCES = ["proj.cpp", "stream.hip", "gemm.hip", "gemv.hip", "generic.hip",
-           "decode.cpp", "quant.hip", "kvcache.hip", "attend.hip"]
+           "decode.cpp", "quant.hip", "kvcache.hip", "attend.hip", "layer.cpp", "int8.hip",
+           "prefix.hip"]
 
 
 def hipcc() -> str:

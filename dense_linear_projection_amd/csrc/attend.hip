@@ -101,13 +101,16 @@ struct AttendCfg {
     }
 };
 
-// First token of a sequence that is seen, and how many parts its tokens make.
+// Of a sequence of n tokens, the first a.prefix of which are another kernel's
+// (none, unless the batch shares them): the first of its own that is seen, and
+// how many parts its own tokens make.
 __device__ __forceinline__ int64_t first_seen(const AttendArgs &a, int64_t n) {
-    return a.window > 0 && n > a.window ? n - a.window : 0;
+    const int64_t first = (a.window > 0 && n > a.window ? n - a.window : 0) - a.prefix;
+    return first > 0 ? first : 0;
 }
 __device__ __forceinline__ int parts_of(const AttendArgs &a, int64_t n) {
-    if (n <= 0 || n > a.max_len) return 0;
-    return static_cast<int>((n - first_seen(a, n) + a.part - 1) / a.part);
+    if (n <= a.prefix || n > a.max_len) return 0;
+    return static_cast<int>((n - a.prefix - first_seen(a, n) + a.part - 1) / a.part);
 }
 
 // Four elements of a finished head (and, with the first, its logarithm of the sum).
@@ -171,7 +174,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
     const int parts = parts_of(a, n);
     if (part >= (parts > 0 ? parts : 1)) return;
     const int64_t first = first_seen(a, n) + part * a.part;
-    const int64_t last = parts == 0 ? first : n < first + a.part ? n : first + a.part;
+    const int64_t last = parts == 0 ? first : n - a.prefix < first + a.part ? n - a.prefix : first + a.part;
     if (tid == 0) wrong = n < 0 || n > a.max_len;
 
     bf16x8 q[QT][C::KS];
@@ -396,8 +399,8 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                 v = f32x4{nan, nan, nan, nan};
             }
             const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + q0 + 16 * t + hq;
-            if (parts > 1) {
-                float *to = a.ws + (row * a.parts + part) * (D + 4);
+            if (parts > 1 || a.prefix_parts > 0) {
+                float *to = a.ws + (row * (a.parts + a.prefix_parts) + part) * (D + 4);
                 put_part(to + d, v[0], v[1], a.join);
                 put_part(to + d + 2, v[2], v[3], a.join);
                 if (d == 0) put_part(to + D, most, total, a.join);
@@ -446,18 +449,23 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
 }
 
 // Joins the parts of one sequence's head: D / 4 threads over the elements,
-// the rest over the parts.
+// the rest over the parts. Those of a shared prefix lie behind a.parts of the
+// sequence's own, of which the first is there also for a sequence without tokens.
 template <int D>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     constexpr int COLS = D / 4, SLICES = 256 / COLS;
     __shared__ float red[SLICES][D + 4], peak[4];
     const int64_t row = blockIdx.x;
-    const int parts = parts_of(a, a.lengths[row / a.q_heads]);
-    if (parts <= 1) return;  // written by its only part
-    const float *from = a.ws + row * a.parts * (D + 4);
+    const int64_t n = a.lengths[row / a.q_heads];
+    int own = parts_of(a, n);
+    if (a.prefix_parts == 0 && own <= 1) return;  // written by its only part
+    if (own == 0 && a.parts > 0) own = 1;
+    const int parts = own + a.prefix_parts;
+    const float *from = a.ws + row * (a.parts + a.prefix_parts) * (D + 4);
+    auto place = [&](int p) -> int64_t { return (p < own ? p : p - own + a.parts) * (D + 4); };
     const int tid = threadIdx.x;
     float most = kLowest;
-    for (int p = tid; p < parts; p += 256) most = fmaxf(most, from[p * (D + 4) + D]);
+    for (int p = tid; p < parts; p += 256) most = fmaxf(most, from[place(p) + D]);
 #pragma unroll
     for (int x = 32; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor(most, x, 64));
     if ((tid & 63) == 0) peak[tid >> 6] = most;
@@ -468,7 +476,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
         float total = 0.f;
         for (int p = slice; p < parts; p += SLICES) {
-            const float *x = from + static_cast<int64_t>(p) * (D + 4);
+            const float *x = from + place(p);
             const float f = exp_above(x[D], most);
             v += *reinterpret_cast<const f32x4 *>(x + d) * f;
             total += x[D + 1] * f;
@@ -484,6 +492,10 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     for (int s = 0; s < SLICES; ++s) {
         v += *reinterpret_cast<const f32x4 *>(&red[s][d]);
         total += red[s][D];
+    }
+    if (n < 0 || n > a.max_len) {
+        total = __builtin_nanf("");
+        v = f32x4{total, total, total, total};
     }
     finish_head(a, row * D + d, row, d, v, most, total);
 }
@@ -512,29 +524,19 @@ bool attend_dim(int dim) {
     return dim == 64 || dim == 80 || dim == 96 || dim == 128 || dim == 192 || dim == 256;
 }
 
-template <int D>
-static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
-    // two tiles of 16 query heads to a workgroup where their outputs fit its
-    // registers; else another workgroup reads the same keys and values
-    constexpr bool kTwo = D <= 128;
-    const int per = a.q_heads / a.c.heads, qt = kTwo && per > 16 ? 2 : 1;
-    a.chunks = (per + 16 * qt - 1) / (16 * qt);
-    const int64_t hh = static_cast<int64_t>(a.c.heads) * a.chunks, rows = a.B * hh, most_rows = most_groups(256) - 7 * hh;
-    if (a.B > 1 && (rows > most_rows || a.B * a.q_heads > most_groups(256))) {
-        // more than one launch can have workgroups for: half the sequences at a time
-        AttendArgs x = a, y = a;
-        x.B = a.B / 2;
-        y.B = a.B - x.B;
-        y.q = a.q + x.B * a.q_stride;
-        y.tables = a.tables + x.B * a.table_stride;
-        y.lengths = a.lengths + x.B;
-        const int64_t heads = x.B * a.q_heads;
-        y.out = static_cast<char *>(a.out) + heads * D * (a.out_dtype == OUT_F32 ? 4 : 2);
-        y.lse = a.lse ? a.lse + heads : nullptr;
-        const hipError_t e = launch_attend_dim<D>(x, st);
-        return e != hipSuccess ? e : launch_attend_dim<D>(y, st);
-    }
-    const int64_t span = a.window > 0 && a.window < a.max_len ? a.window : a.max_len;
+// Two tiles of 16 query heads to a workgroup where their outputs fit its
+// registers; else another workgroup reads the same keys and values.
+static int head_tiles(const AttendArgs &a) { return a.c.dim <= 128 && a.q_heads / a.c.heads > 16 ? 2 : 1; }
+
+int attend_chunks(const AttendArgs &a) {
+    const int qt = head_tiles(a);
+    return (a.q_heads / a.c.heads + 16 * qt - 1) / (16 * qt);
+}
+
+// Sets a.part and a.parts for sequences of up to `longest` own tokens, `room` parts at most.
+void plan_attend(AttendArgs &a, int64_t longest, int64_t room) {
+    const int64_t rows = a.B * a.c.heads * a.chunks;
+    const int64_t span = a.window > 0 && a.window < longest ? a.window : longest;
     // Parts of the length: enough workgroups for four to a compute unit, none
     // shorter than one tile for each wave, and none so long that units idle at
     // the end where lengths differ.  One sequence has parts of one length: all
@@ -543,9 +545,6 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     int64_t part = (span * rows + want - 1) / want;
     part = part < 128 ? 128 : part > most ? most : (part + 127) / 128 * 128;
     int64_t parts = span > part ? (span + part - 1) / part : 1;
-    // no more than the workspace holds and one launch can have
-    const int64_t held = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
-    const int64_t room = held < most_rows / rows ? held : most_rows / rows;
     if (parts > 1 && parts > room) {
         parts = room < 1 ? 1 : room;
         part = ((span + parts - 1) / parts + 127) / 128 * 128;
@@ -554,43 +553,85 @@ static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
     if (parts == 1) part = span > 0 ? span : 1;
     a.part = part;
     a.parts = static_cast<int>(parts);
-    // few parts are joined by the last workgroup; for many, one workgroup to
-    // each sequence's head is faster and the launch is hidden by the first kernel
-    a.join = parts > 1 && parts <= kJoined && rows <= a.ncounters;
+}
+
+// One launch of attend_kernel for the parts that are planned.
+template <int D>
+static hipError_t enqueue_attend(AttendArgs a, hipStream_t st) {
+    const int64_t hh = static_cast<int64_t>(a.c.heads) * a.chunks;
     // Heads between a head's tokens (token-major pages): neighbouring heads'
     // rows may share 128-byte lines
     const int64_t size = a.c.fp8 ? 1 : 2;
     const bool mixed = a.c.kt != D || a.c.vt != D;
     const bool once = !mixed || (D * size % 128 == 0 && (a.c.kt | a.c.vt | a.c.kh | a.c.vh) * size % 128 == 0 &&
                                  (reinterpret_cast<uintptr_t>(a.c.k) | reinterpret_cast<uintptr_t>(a.c.v)) % 128 == 0);
-    a.by_die = mixed && a.B * parts >= 8;
-    const int64_t grid = a.by_die ? (a.B * parts + 7) / 8 * 8 * hh : rows * parts;
+    a.by_die = mixed && a.B * a.parts >= 8;
+    const int64_t grid = a.by_die ? (a.B * a.parts + 7) / 8 * 8 * hh : a.B * hh * a.parts;
     auto pick = [&](auto two) {
         constexpr int QT = decltype(two)::value;
         if (a.c.fp8) return once ? attend_kernel<D, true, QT, true> : attend_kernel<D, true, QT, false>;
         return once ? attend_kernel<D, false, QT, true> : attend_kernel<D, false, QT, false>;
     };
     auto kernel = pick(std::integral_constant<int, 1>());
-    if constexpr (kTwo)
-        if (qt == 2) kernel = pick(std::integral_constant<int, 2>());
+    if constexpr (D <= 128)
+        if (head_tiles(a) == 2) kernel = pick(std::integral_constant<int, 2>());
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || parts == 1 || a.join) return e;
+    return hipGetLastError();
+}
+
+template <int D>
+static hipError_t enqueue_join(const AttendArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((attend_join_kernel<D>), dim3(static_cast<unsigned>(a.B * a.q_heads)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
-hipError_t launch_attend(const AttendArgs &a, hipStream_t st) {
-    switch (a.c.dim) {
-        case 64: return launch_attend_dim<64>(a, st);
-        case 80: return launch_attend_dim<80>(a, st);
-        case 96: return launch_attend_dim<96>(a, st);
-        case 128: return launch_attend_dim<128>(a, st);
-        case 192: return launch_attend_dim<192>(a, st);
-        case 256: return launch_attend_dim<256>(a, st);
-    }
-    return hipErrorInvalidValue;
+// The second half of a batch whose first has `first` sequences.
+AttendArgs attend_rest(const AttendArgs &a, int64_t first) {
+    AttendArgs y = a;
+    y.B = a.B - first;
+    y.q = a.q + first * a.q_stride;
+    y.tables = a.tables + first * a.table_stride;
+    y.lengths = a.lengths + first;
+    const int64_t heads = first * a.q_heads;
+    y.out = static_cast<char *>(a.out) + heads * a.c.dim * (a.out_dtype == OUT_F32 ? 4 : 2);
+    y.lse = a.lse ? a.lse + heads : nullptr;
+    return y;
 }
+
+template <int D>
+static hipError_t launch_attend_dim(AttendArgs a, hipStream_t st) {
+    a.chunks = attend_chunks(a);
+    const int64_t hh = static_cast<int64_t>(a.c.heads) * a.chunks, rows = a.B * hh, most_rows = most_groups(256) - 7 * hh;
+    if (a.B > 1 && (rows > most_rows || a.B * a.q_heads > most_groups(256))) {
+        // more than one launch can have workgroups for: half the sequences at a time
+        AttendArgs x = a;
+        x.B = a.B / 2;
+        const hipError_t e = launch_attend_dim<D>(x, st);
+        return e != hipSuccess ? e : launch_attend_dim<D>(attend_rest(a, x.B), st);
+    }
+    // no more than the workspace holds and one launch can have
+    const int64_t held = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
+    plan_attend(a, a.max_len, held < most_rows / rows ? held : most_rows / rows);
+    // few parts are joined by the last workgroup; for many, one workgroup to
+    // each sequence's head is faster and the launch is hidden by the first kernel
+    a.join = a.parts > 1 && a.parts <= kJoined && rows <= a.ncounters;
+    const hipError_t e = enqueue_attend<D>(a, st);
+    return e != hipSuccess || a.parts == 1 || a.join ? e : enqueue_join<D>(a, st);
+}
+
+#define PROJ_ATTEND_DIMS(F)                  \
+    switch (a.c.dim) {                       \
+        case 64: return F<64>(a, st);        \
+        case 80: return F<80>(a, st);        \
+        case 96: return F<96>(a, st);        \
+        case 128: return F<128>(a, st);      \
+        case 192: return F<192>(a, st);      \
+        case 256: return F<256>(a, st);      \
+    }                                        \
+    return hipErrorInvalidValue;
+hipError_t launch_attend(const AttendArgs &a, hipStream_t st) { PROJ_ATTEND_DIMS(launch_attend_dim) }
+hipError_t launch_attend_parts(const AttendArgs &a, hipStream_t st) { PROJ_ATTEND_DIMS(enqueue_attend) }
+hipError_t launch_attend_join(const AttendArgs &a, hipStream_t st) { PROJ_ATTEND_DIMS(enqueue_join) }
 #endif
 
 }  // namespace proj

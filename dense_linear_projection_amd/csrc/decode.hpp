@@ -54,6 +54,11 @@ struct AppendArgs {
     const int32_t *positions;
     const int64_t *slots;
     uint16_t *q_out;
+    // weights of the heads' norms, bf16 or fp32 (nullptr: no norm), [head_dim] or [heads][head_dim]
+    const void *q_norm = nullptr, *k_norm = nullptr;
+    int norm_f32 = 0, norm_per_head = 0;
+    float eps = 0.f;
+    int norm_lanes = 0;  // set by the launcher: lanes of a head
 };
 hipError_t launch_append(const AppendArgs &a, hipStream_t st);
 
@@ -80,8 +85,20 @@ struct AttendArgs {
     // workgroup to finish joins its parts, whether a part's heads go to one die
     int64_t part = 0;
     int parts = 0, chunks = 0, join = 0, by_die = 0;
+    // where the batch shares its first tokens (prefix.hip): how many, and the
+    // parts of them that lie behind a row's own in the workspace
+    int prefix_parts = 0;
+    int64_t prefix = 0;
 };
 hipError_t launch_attend(const AttendArgs &a, hipStream_t st);
+// Its steps, for a batch with a shared prefix: workgroups that a key-value head's query heads need; the split
+// of `longest` own tokens into at most `room` parts; the kernel of the parts, and that which joins them; the
+// arguments of a batch behind its first sequences.
+int attend_chunks(const AttendArgs &a);
+void plan_attend(AttendArgs &a, int64_t longest, int64_t room);
+hipError_t launch_attend_parts(const AttendArgs &a, hipStream_t st);
+hipError_t launch_attend_join(const AttendArgs &a, hipStream_t st);
+AttendArgs attend_rest(const AttendArgs &a, int64_t first);
 bool attend_dim(int dim);  // whether a kernel for this head size is built
 
 }  // namespace proj

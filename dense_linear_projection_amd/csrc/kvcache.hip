@@ -1,5 +1,5 @@
-// kvcache.hip -- rotary positions and the storing of keys and values into a
-// paged key-value cache.
+// kvcache.hip -- norms of query and key heads, rotary positions and the storing
+// of keys and values into a paged key-value cache.
 #include "decode.hpp"
 
 namespace proj {
@@ -47,19 +47,43 @@ __device__ __forceinline__ void store8_fp8(uint8_t *p, const float *x, float sca
     *reinterpret_cast<u32x2 *>(p) = w;
 }
 
+// A norm's weights of an item's eight elements.
+__device__ __forceinline__ void load8_weights(const AppendArgs &a, const void *norm, int64_t at, float *w) {
+    if (a.norm_f32) {
+        const float *p = static_cast<const float *>(norm) + at;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(p + 4 * v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[4 * v + k] = x[k];
+        }
+    } else {
+        load8(static_cast<const uint16_t *>(norm) + at, w);
+    }
+}
+
 // A thread has one item of TOK tokens, T / TOK apart in no order that
 // matters: their loads are in flight together, and the item's head and place
 // are worked out once.  Bound by bytes: each is read and written once, the
 // table's rows come from the caches; 8192 tokens of 80 heads of 128 into an 8-bit
 // cache 64.5 us, 5.0 TB/s, a copy's rate (an element to a thread: 203 us).
-template <int PAIRING, int TOK>
+//
+// NORM: a query or key head is first divided by the root of its mean square
+// (plus eps) and multiplied by its weights. A head's items are then neighbouring
+// lanes of one wave, 4, 8 or 16 of them (those past D / 16 have no elements), and
+// exchange their sums. Squares, their sum and the root are held in 64 bits: no
+// bf16 input overflows or vanishes there.
+template <int PAIRING, int TOK, bool NORM>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t blocks) {
-    const int D = a.c.dim, per = D / 16;
+    const int D = a.c.dim, per = NORM ? a.norm_lanes : D / 16;
     const int item = static_cast<int>(blockIdx.x % blocks) * 256 + threadIdx.x;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x / blocks) * TOK;
-    const int head = item / per, c = item % per, Hq = a.q_heads, Hkv = a.c.heads;
+    const int head = item / per, Hq = a.q_heads, Hkv = a.c.heads;
+    int c = item % per;
     const int kind = head < Hq ? 0 : head < Hq + Hkv ? 1 : 2;  // query, key, value
     if (head >= Hq + 2 * Hkv || (kind == 0 && !a.q_out)) return;
+    const bool idle = NORM && c >= D / 16;  // a lane that only takes part in the exchange
+    if (idle) c = D / 16 - 1;
     const int half = a.rot / 2;
     // the item's two runs of eight, and whether they are rotated
     int e0 = 16 * c, e1 = 16 * c + 8;
@@ -72,6 +96,13 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t bloc
         }
     }
     const uint16_t *row = a.qkv + t0 * a.stride + static_cast<int64_t>(head) * D;
+    const void *norm = !NORM || kind == 2 ? nullptr : kind == 0 ? a.q_norm : a.k_norm;
+    const int64_t norm_at = a.norm_per_head ? static_cast<int64_t>(kind == 0 ? head : head - Hq) * D : 0;
+    float weight[2][8];
+    if (NORM && norm) {
+        load8_weights(a, norm, norm_at + e0, weight[0]);
+        load8_weights(a, norm, norm_at + e1, weight[1]);
+    }
 
     float x[TOK][2][8];
     int64_t slot[TOK];
@@ -89,6 +120,19 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t bloc
         if (t0 + i >= a.T) break;
         const bool known = a.rot == 0 || (pos[i] >= 0 && pos[i] < a.rope_rows);
         const float *cs = a.rope + static_cast<int64_t>(known ? pos[i] : 0) * a.rot;
+        double root = 1.0;  // 1 / sqrt(mean square + eps) of the head
+        if (NORM && norm) {
+            double sum = 0.0;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum = __builtin_fma(x[i][k / 8][k % 8], static_cast<double>(x[i][k / 8][k % 8]), sum);
+            if (idle) sum = 0.0;
+            for (int h = 1; h < per; h <<= 1) sum += __shfl_xor(sum, h, 64);
+            const double mean = sum / D + static_cast<double>(a.eps);
+            root = 1.0 / sqrt(mean);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                x[i][k / 8][k % 8] = static_cast<float>(x[i][k / 8][k % 8] * root) * weight[k / 8][k % 8];
+        }
         if (turns && known) {
             if constexpr (PAIRING == kHalves) {
 #pragma unroll
@@ -124,12 +168,18 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t bloc
                             const int j = a.interleaved ? d >> 1 : d < half ? d : d - half;
                             const bool second = a.interleaved ? (d & 1) != 0 : d >= half;
                             const int partner = a.interleaved ? d ^ 1 : second ? d - half : d + half;
-                            const float u = bf16_bits_to_f32(row[i * a.stride + partner]), co = cs[j], si = cs[half + j];
+                            float u = bf16_bits_to_f32(row[i * a.stride + partner]);
+                            if (NORM && norm)
+                                u = static_cast<float>(u * root) *
+                                    (a.norm_f32 ? static_cast<const float *>(norm)[norm_at + partner]
+                                                : bf16_bits_to_f32(static_cast<const uint16_t *>(norm)[norm_at + partner]));
+                            const float co = cs[j], si = cs[half + j];
                             x[i][v][k] = second ? x[i][v][k] * co + u * si : x[i][v][k] * co - u * si;
                         }
                     }
             }
         }
+        if (idle) continue;
         if (kind == 0) {
             if (!known)
 #pragma unroll
@@ -158,20 +208,23 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t bloc
 }
 
 #define PROJ_APPEND_INST(P)                                                    \
-    template __global__ void append_kernel<P, 1>(AppendArgs, uint32_t);        \
-    template __global__ void append_kernel<P, 4>(AppendArgs, uint32_t);
+    template __global__ void append_kernel<P, 1, false>(AppendArgs, uint32_t); \
+    template __global__ void append_kernel<P, 4, false>(AppendArgs, uint32_t); \
+    template __global__ void append_kernel<P, 1, true>(AppendArgs, uint32_t);  \
+    template __global__ void append_kernel<P, 4, true>(AppendArgs, uint32_t);
 PROJ_APPEND_INST(kHalves)
 PROJ_APPEND_INST(kNeighbours)
 PROJ_APPEND_INST(kAny)
 
 #ifndef __HIP_DEVICE_COMPILE__
-template <int PAIRING>
-static hipError_t launch_append_as(const AppendArgs &a, hipStream_t st) {
-    const int64_t items = (static_cast<int64_t>(a.q_heads) + 2 * a.c.heads) * (a.c.dim / 16);
+template <int PAIRING, bool NORM>
+static hipError_t launch_append_as(AppendArgs a, hipStream_t st) {
+    a.norm_lanes = a.c.dim <= 64 ? 4 : a.c.dim <= 128 ? 8 : 16;
+    const int64_t items = (static_cast<int64_t>(a.q_heads) + 2 * a.c.heads) * (NORM ? a.norm_lanes : a.c.dim / 16);
     const int64_t blocks = (items + 255) / 256;
     // four tokens to a thread once that leaves enough threads for the chip
     const int tok = a.T * items >= (int64_t{1} << 20) ? 4 : 1;
-    auto kernel = tok == 4 ? append_kernel<PAIRING, 4> : append_kernel<PAIRING, 1>;
+    auto kernel = tok == 4 ? append_kernel<PAIRING, 4, NORM> : append_kernel<PAIRING, 1, NORM>;
     // as many tokens at a time as one launch can have threads for
     const int64_t most = most_groups(256) / blocks * tok;
     AppendArgs s = a;
@@ -189,9 +242,14 @@ static hipError_t launch_append_as(const AppendArgs &a, hipStream_t st) {
     return hipSuccess;
 }
 
+template <bool NORM>
+static hipError_t launch_append_norm(const AppendArgs &a, hipStream_t st) {
+    if (a.rot % 16 != 0 || reinterpret_cast<uintptr_t>(a.rope) % 16 != 0) return launch_append_as<kAny, NORM>(a, st);
+    return a.interleaved ? launch_append_as<kNeighbours, NORM>(a, st) : launch_append_as<kHalves, NORM>(a, st);
+}
+
 hipError_t launch_append(const AppendArgs &a, hipStream_t st) {
-    if (a.rot % 16 != 0 || reinterpret_cast<uintptr_t>(a.rope) % 16 != 0) return launch_append_as<kAny>(a, st);
-    return a.interleaved ? launch_append_as<kNeighbours>(a, st) : launch_append_as<kHalves>(a, st);
+    return a.q_norm || a.k_norm ? launch_append_norm<true>(a, st) : launch_append_norm<false>(a, st);
 }
 #endif
 

@@ -303,6 +303,47 @@ proj_status proj_run_quant(proj_ctx *ctx, const void *X, const uint32_t *codes, 
                            const uint8_t *zeros, int group, const void *bias, int epilogue, int64_t M, int64_t N,
                            int64_t K, void *Y, int out_dtype, void *stream);
 
+/* ---- 8-bit integers with a scale for each token and each output (what bounds a
+ * prompt's projection is the matrix rate, twice that of bf16; what bounds a
+ * decoding step's is the weights' bytes, half those of bf16).
+ *
+ * proj_quantize_rows makes them from bf16 rows, tokens and weights alike:
+ * scales[m] = max_k |X[m, k]| / 127 (fp32) and q[m, k] = rint(127 X[m, k] /
+ * max_k |X[m, k]|), the exact quotient rounded to nearest even; a row of zeros
+ * has scale 0, one with a NaN or an infinity scale NaN, both codes 0. X row m
+ * starts at X + m * x_stride (x_stride >= K; rows that start at 16-byte
+ * boundaries are read faster), q row m at q + m * q_stride: q is 16-byte
+ * aligned, q_stride a multiple of 16 and at least K, and columns K ..
+ * q_stride - 1 are written zero, which is how a K that is not a multiple of 16
+ * meets the product below. */
+proj_status proj_quantize_rows(proj_ctx *ctx, const void *X, int64_t x_stride, int64_t M, int64_t K, int8_t *q,
+                               int64_t q_stride, float *scales, void *stream);
+
+/* Y = epilogue(x_scales[m] w_scales[n] sum_k X[m, k] W[n, k] (+ bias)) for X
+ * int8 [M][K] and W int8 [N][K], 16-byte aligned, K a multiple of 16
+ * (PROJ_ERR_INVALID_ARG otherwise) and at most 131056 (PROJ_ERR_UNSUPPORTED
+ * beyond: 2^17 products of -128 and -128 pass 32 bits); scales fp32. The sum is
+ * exact; it is multiplied by both scales in 64-bit floating point and rounded to
+ * fp32 once, then bias and GELU follow as in proj_run. Epilogue, output types,
+ * M = 0, N = 0, K = 0 and overlap rules as proj_run. Allocates nothing and never
+ * synchronises, so it may be captured; which kernel runs follows from the sizes
+ * (and how far K is split from the context's workspace, which holds the 32-bit
+ * sums of a split K): every kernel gives the same bits. */
+proj_status proj_run_int(proj_ctx *ctx, const int8_t *X, const float *x_scales, const int8_t *W, const float *w_scales,
+                         const void *bias, int epilogue, int64_t M, int64_t N, int64_t K, void *Y, int out_dtype,
+                         void *stream);
+
+/* The same from bf16 tokens X [M][K] (rows x_stride apart), made integers as by
+ * proj_quantize_rows: the result is that of the two calls. W int8 [N][K rounded
+ * up to a multiple of 16], zero behind K, as proj_quantize_rows writes it. The
+ * tokens' integers lie in the context's workspace, as many rows at a time as it
+ * holds; PROJ_ERR_NO_MEMORY (nothing enqueued) where it does not hold one: K + 4
+ * bytes, K rounded up, and 512. A token that meets several projections is made
+ * integers once with proj_quantize_rows instead. */
+proj_status proj_run_int_dynamic(proj_ctx *ctx, const void *X, int64_t x_stride, const int8_t *W, const float *w_scales,
+                                 const void *bias, int epilogue, int64_t M, int64_t N, int64_t K, void *Y, int out_dtype,
+                                 void *stream);
+
 /* ---- Paged key-value cache: what runs between a decoding step's QKV
  * projection and its output projection.
  *
@@ -349,6 +390,20 @@ proj_status proj_kv_append(proj_ctx *ctx, const proj_kv_cache *cache, const void
                            int q_heads, const float *rope, int64_t rope_rows, int rot, int interleaved,
                            const int32_t *positions, const int64_t *slots, void *q_out, void *stream);
 
+/* proj_kv_append whose query and key heads are normed before they are rotated:
+ * a head x becomes x[d] / sqrt(mean_d x[d]^2 + eps) * w[d], with w = q_norm for
+ * the query heads and k_norm for the key heads (NULL: those are not normed;
+ * values never are), bf16 or fp32 (norm_dtype, a proj_out_dtype), 16-byte
+ * aligned, [head_dim] for every head or, with norm_per_head, [q_heads][head_dim]
+ * and [heads][head_dim]. The mean and the root are 64-bit, the result fp32 and
+ * rounded where it is stored. eps is finite and not negative; with eps = 0 a head
+ * of zeros is NaN, as the formula is. A NaN in a head makes the head NaN. The
+ * weights may not overlap q_out or the cache. */
+proj_status proj_kv_append_norm(proj_ctx *ctx, const proj_kv_cache *cache, const void *qkv, int64_t qkv_stride, int64_t T,
+                                int q_heads, const void *q_norm, const void *k_norm, int norm_dtype, int norm_per_head,
+                                float eps, const float *rope, int64_t rope_rows, int rot, int interleaved,
+                                const int32_t *positions, const int64_t *slots, void *q_out, void *stream);
+
 /* Attention of one new token for each of B sequences over its pages: query
  * head h reads key-value head h / (q_heads / cache->heads);
  *     w[t] = scale * <q, k[t]>,  out = sum_t softmax(w)[t] v[t],
@@ -373,6 +428,26 @@ proj_status proj_kv_attend(proj_ctx *ctx, const proj_kv_cache *cache, const void
                            int q_heads, const int32_t *tables, int64_t table_stride, int64_t table_width,
                            const int32_t *lengths, int64_t max_len, int64_t window, float scale, void *out,
                            int out_dtype, float *lse, void *stream);
+
+/* The same for a batch whose sequences begin with the same tokens, stored once:
+ * token t < prefix_len of every sequence is in page prefix[t / page_size], place
+ * t % page_size; token t >= prefix_len of sequence b is token t - prefix_len of
+ * its own, in page tables[b * table_stride + (t - prefix_len) / page_size].
+ * prefix_len need not be a multiple of page_size. lengths, max_len and window
+ * count all of a sequence's tokens, so a length below prefix_len sees that much
+ * of the prefix; the tables hold max_len - prefix_len tokens at least. Each key
+ * and value of the prefix is read once for groups of 128 query rows of the
+ * batch, not once for every sequence. Definition, types, alignment, padding
+ * places and errors otherwise as proj_kv_attend; a page of the prefix outside
+ * the cache makes those sequences NaN that see a token of it. Probabilities of
+ * the prefix meet the values with 24 bits for fp32 results and with 16 for bf16
+ * ones, which have 8. The workspace holds the fp32 results of the prefix's and
+ * the sequences' parts: PROJ_ERR_NO_MEMORY (nothing enqueued) where it does not
+ * hold two of (head_dim + 4) * 4 bytes for every query head of one sequence. */
+proj_status proj_kv_attend_shared(proj_ctx *ctx, const proj_kv_cache *cache, const void *q, int64_t q_stride, int64_t B,
+                                  int q_heads, const int32_t *prefix, int64_t prefix_len, const int32_t *tables,
+                                  int64_t table_stride, int64_t table_width, const int32_t *lengths, int64_t max_len,
+                                  int64_t window, float scale, void *out, int out_dtype, float *lse, void *stream);
 
 /* Free the context's device memory and plans (synchronises its device
  * first).  The handle itself stays allocated (a few hundred bytes) as a
