@@ -74,34 +74,205 @@ __device__ __forceinline__ float scaled(int32_t sum, float xs, float ws) {
     return static_cast<float>(static_cast<double>(sum) * (static_cast<double>(xs) * ws));
 }
 
-// 16 x 16 outputs to a wave, operands straight from memory.
-__global__ __launch_bounds__(256) void int_wave_kernel(IntArgs a) {
-    const int lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
-    const int64_t tn = (a.N + 15) / 16, tiles = tn * ((a.M + 15) / 16);
-    for (int64_t tile = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); tile < tiles;
-         tile += static_cast<int64_t>(gridDim.x) * 4) {
-        const int64_t m = tile / tn * 16 + c16, n = tile % tn * 16 + c16;
-        const int8_t *x = a.X + (m < a.M ? m : a.M - 1) * a.K, *w = a.W + (n < a.N ? n : a.N - 1) * a.K;
-        i32x4 acc = {0, 0, 0, 0};
-        for (int64_t k = 0; k < a.K; k += 64) {
-            i32x4 xv = {0, 0, 0, 0}, wv = {0, 0, 0, 0};
-            if (k + 16 * g < a.K) {
-                xv = *reinterpret_cast<const i32x4 *>(x + k + 16 * g);
-                wv = *reinterpret_cast<const i32x4 *>(w + k + 16 * g);
-            }
-            acc = mfma16x16x64(wv, xv, acc);
-        }
-        if (m >= a.M) continue;
+// Four outputs of one token, before bias and GELU scaled already, written where they are there.
+__device__ __forceinline__ void write4(const IntArgs &a, int64_t m, int64_t n, const int32_t (&sum)[4], float xs) {
+    float v[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t col = tile % tn * 16 + 4 * g + r;
-            if (col >= a.N) continue;
-            const float b = (a.epi & 1) ? bf16_bits_to_f32(a.bias[col]) : 0.f;
-            const float s = a.K > 0 ? scaled(acc[r], a.x_scales[m], a.w_scales[col]) : 0.f;
-            store_out(a.Y, a.out, m * a.N + col, apply_epilogue(s, a.epi, b));
+    for (int r = 0; r < 4; ++r) {
+        const int64_t col = n + r < a.N ? n + r : a.N - 1;
+        v[r] = apply_epilogue(scaled(sum[r], xs, a.w_scales[col]), a.epi, (a.epi & 1) ? bf16_bits_to_f32(a.bias[col]) : 0.f);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (n + r < a.N) store_out(a.Y, a.out, m * a.row + n + r, v[r]);
+}
+
+// An offset past every resource made here (they are below 2^31 bytes): a load there gives zero.
+constexpr uint32_t kOutside = 0x80000000u;
+
+// Few tokens: bound by reading W once. A workgroup has 16 MT tokens and 16 NT
+// outputs and walks its share of K in stages of KC bytes, D - 1 of them on
+// their way into an LDS ring (global-to-LDS copies of 1 KB, whole runs of KC bytes of
+// a row) while one is multiplied; wave w takes the 64-byte steps w, w + WAVES, ...
+// of a stage for the whole tile, and the waves' sums meet in LDS at the end.
+// 16-byte chunk c of LDS row r lies at position c ^ (r % 16): the 16 rows of a
+// fragment fall on different banks. W is read past the caches (non-temporal), X
+// stays in them. With S > 1 splits of K the last workgroup of a tile to
+// finish adds the others' sums, which lie in the workspace.
+template <int MT, int NT, int WAVES, int KC, int D>
+struct IntStreamCfg {
+    static constexpr int NR = 16 * NT, MR = 16 * MT, CPR = KC / 16, RPI = 1024 / KC;
+    static constexpr int STAGE = (NR + MR) * KC;
+    static constexpr int PERW = STAGE / 1024 / WAVES;    // copies of a wave in a stage
+    static constexpr int E = MT * NT * 256;              // outputs of a tile
+    static constexpr int RED = WAVES * E * 4;
+    static constexpr int LDS = D * STAGE > RED ? D * STAGE : RED;
+    static_assert(STAGE % (1024 * WAVES) == 0 && CPR >= 16 && KC / 64 >= WAVES && (KC / 64) % WAVES == 0, "stage");
+    static_assert(PERW * (D - 2) <= 63 && LDS <= 160 * 1024, "ring");
+};
+
+template <int MT, int NT, int WAVES, int KC, int D>
+__global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint32_t splits) {
+    using C = IntStreamCfg<MT, NT, WAVES, KC, D>;
+    __shared__ __attribute__((aligned(16))) char lds[C::LDS];
+    const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t tiles_n = static_cast<uint32_t>((a.N + C::NR - 1) / C::NR);
+    uint32_t tile = blockIdx.x, split = 0;
+    if (splits > 1) {
+        tile = blockIdx.x / splits;
+        split = blockIdx.x - tile * splits;
+    }
+    uint32_t tm = 0, tn = tile;
+    if (a.M > C::MR) {
+        tm = tile / tiles_n;
+        tn = tile - tm * tiles_n;
+    }
+    const int64_t m0 = static_cast<int64_t>(tm) * C::MR, n0 = static_cast<int64_t>(tn) * C::NR;
+    const int K = static_cast<int>(a.K), T = (K + KC - 1) / KC;
+    const int first = static_cast<int>(static_cast<uint32_t>(T) * split / splits);
+    const int nst = static_cast<int>(static_cast<uint32_t>(T) * (split + 1) / splits) - first;
+    // Workgroups begin at different places of K: rows lie a power of two apart, and walking in step would
+    // gather all reads on few memory channels.
+    const int turn = nst > 0 ? static_cast<int>(tn * 7u % static_cast<uint32_t>(nst)) : 0;
+
+    const int64_t rows_w = a.N - n0 < C::NR ? a.N - n0 : C::NR, rows_x = a.M - m0 < C::MR ? a.M - m0 : C::MR;
+    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.W + n0 * a.K, static_cast<uint32_t>(rows_w * a.K));
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X + m0 * a.K, static_cast<uint32_t>(rows_x * a.K));
+    const __amdgpu_buffer_rsrc_t none = buffer_rsrc(a.X, 0);
+    uint32_t voff[C::PERW];
+    int chunk[C::PERW];
+#pragma unroll
+    for (int j = 0; j < C::PERW; ++j) {
+        const int row = (wave + j * WAVES) * C::RPI + lane / C::CPR;
+        chunk[j] = ((lane % C::CPR) ^ (row & 15)) * 16;
+        voff[j] = static_cast<uint32_t>((row < C::NR ? row : row - C::NR) * K + chunk[j]);
+    }
+    auto issue = [&](int i) {
+        char *slot = lds + (i % D) * C::STAGE;
+        int stage = i + turn;
+        stage = (stage >= nst ? stage - nst : stage) + first;
+        const bool live = i < nst, tail = stage == T - 1 && K % KC != 0;
+#pragma unroll
+        for (int j = 0; j < C::PERW; ++j) {
+            const bool is_w = (wave + j * WAVES) * C::RPI < C::NR;  // wave-uniform
+            // behind K lies the next row
+            const uint32_t v = tail && stage * KC + chunk[j] >= K ? kOutside : voff[j];
+            char *to = slot + (wave + j * WAVES) * 1024;
+            if (is_w)
+                dma16_buf_nt(live ? rw : none, v, static_cast<uint32_t>(stage * KC), to);
+            else
+                dma16_buf(live ? rx : none, v, static_cast<uint32_t>(stage * KC), to);
+        }
+    };
+    i32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) issue(i);
+    for (int i = 0; i < nst; ++i) {
+        wait_vm<C::PERW *(D - 2)>();  // this wave's copies of stage i have landed
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();  // everyone's have, and the slot of stage i - 1 is free
+        asm volatile("" ::: "memory");
+        issue(i + D - 1);
+        const char *slot = lds + (i % D) * C::STAGE;
+#pragma unroll
+        for (int s = 0; s < KC / 64 / WAVES; ++s) {
+            const int c = (wave + s * WAVES) * 4 + g;
+            i32x4 xf[MT], wf[NT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) xf[t] = *reinterpret_cast<const i32x4 *>(slot + (C::NR + t * 16 + c16) * KC + ((c ^ c16) << 4));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) wf[t] = *reinterpret_cast<const i32x4 *>(slot + (t * 16 + c16) * KC + ((c ^ c16) << 4));
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int u = 0; u < NT; ++u) acc[t][u] = mfma16x16x64(wf[u], xf[t], acc[t][u]);
         }
     }
+    wait_vm<0>();
+    __syncthreads();
+
+    // The waves' sums, four outputs (columns 4 g ..) of a token (row c16) at a time
+    i32x4 *red = reinterpret_cast<i32x4 *>(lds);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) red[(wave * MT * NT + t * NT + u) * 64 + lane] = acc[t][u];
+    __syncthreads();
+    constexpr int Q = (C::E / 4 + WAVES * 64 - 1) / (WAVES * 64);
+    i32x4 sum[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int e = tid + q * WAVES * 64;
+        if (e >= C::E / 4) break;
+        sum[q] = red[e];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum[q] += red[w * (C::E / 4) + e];
+    }
+    if (splits > 1) {
+        // Sums go past the dies' own caches, in both directions, so that waiting for the stores is all the order needed.
+        int &is_last = *reinterpret_cast<int *>(lds);  // the sums there are in registers
+        uint64_t *mine = reinterpret_cast<uint64_t *>(a.ws) + (static_cast<int64_t>(tile) * splits + split) * (C::E / 2);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int e = tid + q * WAVES * 64;
+            if (e >= C::E / 4) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                __hip_atomic_store(mine + 2 * e + x, static_cast<uint64_t>(static_cast<uint32_t>(sum[q][2 * x + 1])) << 32 |
+                                                         static_cast<uint32_t>(sum[q][2 * x]),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tid == 0) {
+            is_last = __hip_atomic_fetch_add(a.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == splits;
+            if (is_last) __hip_atomic_store(a.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        if (!is_last) return;
+        const uint64_t *all = reinterpret_cast<const uint64_t *>(a.ws) + static_cast<int64_t>(tile) * splits * (C::E / 2);
+        for (uint32_t p = 0; p < splits; ++p) {
+            if (p == split) continue;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int e = tid + q * WAVES * 64;
+                if (e >= C::E / 4) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint64_t v = __hip_atomic_load(all + p * (C::E / 2) + 2 * e + x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    sum[q][2 * x] += static_cast<int32_t>(static_cast<uint32_t>(v));
+                    sum[q][2 * x + 1] += static_cast<int32_t>(static_cast<uint32_t>(v >> 32));
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int e = tid + q * WAVES * 64;
+        if (e >= C::E / 4) break;
+        const int t = e / 64 / NT, u = e / 64 % NT, ln = e % 64;
+        const int64_t m = m0 + t * 16 + ln % 16, n = n0 + u * 16 + 4 * (ln / 16);
+        if (m >= a.M || n >= a.N) continue;
+        const int32_t v[4] = {sum[q][0], sum[q][1], sum[q][2], sum[q][3]};
+        write4(a, m, n, v, a.x_scales[m]);
+    }
 }
+
+// K = 0: the sum is empty.
+__global__ __launch_bounds__(256) void int_empty_kernel(IntArgs a) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < a.M * a.N; i += static_cast<int64_t>(gridDim.x) * 256)
+        store_out(a.Y, a.out, i, apply_epilogue(0.f, a.epi, (a.epi & 1) ? bf16_bits_to_f32(a.bias[i % a.N]) : 0.f));
+}
+
+#define PROJ_INT_STREAM_VARIANTS(X) \
+    X(1, 1, 4, 256, 9) X(1, 2, 4, 256, 9) X(2, 2, 4, 256, 9) X(4, 2, 4, 256, 6) X(4, 4, 4, 256, 4) X(8, 2, 4, 256, 4) X(8, 4, 4, 256, 3)
+#define PROJ_INT_STREAM_INST(MT, NT, WV, KC, D) template __global__ void int_stream_kernel<MT, NT, WV, KC, D>(IntArgs, uint32_t);
+PROJ_INT_STREAM_VARIANTS(PROJ_INT_STREAM_INST)
 
 #ifndef __HIP_DEVICE_COMPILE__
 hipError_t launch_quantize_rows(const RowsArgs &a, hipStream_t st) {
@@ -110,10 +281,54 @@ hipError_t launch_quantize_rows(const RowsArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-hipError_t launch_int(const IntArgs &a, hipStream_t st) {
-    const int64_t tiles = (a.N + 15) / 16 * ((a.M + 15) / 16), most = most_groups(256), groups = (tiles + 3) / 4;
-    hipLaunchKernelGGL(int_wave_kernel, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(256), 0, st, a);
+template <int MT, int NT, int WAVES, int KC, int D>
+static hipError_t launch_int_stream(const IntArgs &a, hipStream_t st) {
+    using C = IntStreamCfg<MT, NT, WAVES, KC, D>;
+    auto kernel = int_stream_kernel<MT, NT, WAVES, KC, D>;
+    const int64_t tiles = (a.N + C::NR - 1) / C::NR * ((a.M + C::MR - 1) / C::MR), stages = (a.K + KC - 1) / KC;
+    // K is split while there are fewer tiles than compute units, in shares of four stages at least
+    int64_t splits = a.cus / tiles;
+    if (splits > stages / 4) splits = stages / 4;
+    if (splits > static_cast<int64_t>(a.ws_bytes / (C::E * 4)) / tiles) splits = static_cast<int64_t>(a.ws_bytes / (C::E * 4)) / tiles;
+    if (tiles > a.ncounters || splits < 1) splits = 1;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles * splits)), dim3(WAVES * 64), 0, st, a, static_cast<uint32_t>(splits));
     return hipGetLastError();
+}
+
+hipError_t launch_int(const IntArgs &a, hipStream_t st) {
+    const int64_t most = most_groups(256);
+    if (a.K == 0) {
+        const int64_t groups = (a.M * a.N + 255) / 256;
+        hipLaunchKernelGGL(int_empty_kernel, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }
+    // more tiles than one launch can have workgroups for, however small they are: rows, then columns, in pieces
+    if ((a.M + 15) / 16 * ((a.N + 15) / 16) > most) {
+        IntArgs x = a, y = a;
+        const int64_t size = a.out == OUT_F32 ? 4 : 2;
+        if (a.M > 16) {
+            x.M = (a.M / 2 + 15) / 16 * 16;
+            y.M = a.M - x.M;
+            y.X = a.X + x.M * a.K;
+            y.x_scales = a.x_scales + x.M;
+            y.Y = static_cast<char *>(a.Y) + x.M * a.row * size;
+        } else {
+            x.N = (a.N / 2 + 15) / 16 * 16;
+            y.N = a.N - x.N;
+            y.W = a.W + x.N * a.K;
+            y.w_scales = a.w_scales + x.N;
+            y.bias = a.bias ? a.bias + x.N : nullptr;
+            y.Y = static_cast<char *>(a.Y) + x.N * size;
+        }
+        const hipError_t e = launch_int(x, st);
+        return e != hipSuccess ? e : launch_int(y, st);
+    }
+    const int64_t cus = a.cus;
+    auto wide = [&](int nt) { return (a.N + 16 * nt - 1) / (16 * nt) >= cus; };
+    if (a.M <= 16) return wide(2) ? launch_int_stream<1, 2, 4, 256, 9>(a, st) : launch_int_stream<1, 1, 4, 256, 9>(a, st);
+    if (a.M <= 32) return launch_int_stream<2, 2, 4, 256, 9>(a, st);
+    if (a.M <= 64) return wide(4) ? launch_int_stream<4, 4, 4, 256, 4>(a, st) : launch_int_stream<4, 2, 4, 256, 6>(a, st);
+    return wide(4) ? launch_int_stream<8, 4, 4, 256, 3>(a, st) : launch_int_stream<8, 2, 4, 256, 4>(a, st);
 }
 #endif
 

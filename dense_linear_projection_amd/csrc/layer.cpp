@@ -100,8 +100,8 @@ proj_status proj_run_int(proj_ctx *ctx, const int8_t *X, const float *x_scales, 
     if (overlap(Y, yb, X, static_cast<uint64_t>(M) * K) || overlap(Y, yb, x_scales, static_cast<uint64_t>(M) * 4))
         return context_error(ctx, PROJ_ERR_INVALID_ARG, "Y overlaps an input");
     DeviceGuard g(v.device);
-    return finish(ctx, launch_int(IntArgs{X, W, x_scales, w_scales, static_cast<const uint16_t *>(bias), Y, M, N, K, epilogue,
-                                          out_dtype, reinterpret_cast<int32_t *>(v.ws), v.ws_bytes, v.cus},
+    return finish(ctx, launch_int(IntArgs{X, W, x_scales, w_scales, static_cast<const uint16_t *>(bias), Y, M, N, K, N, epilogue,
+                                          out_dtype, reinterpret_cast<int32_t *>(v.ws), v.ws_bytes, v.cus, v.counters, v.ncounters},
                                   static_cast<hipStream_t>(stream)));
 }
 
@@ -138,7 +138,8 @@ proj_status proj_run_int_dynamic(proj_ctx *ctx, const void *X, int64_t x_stride,
         hipError_t e = launch_quantize_rows(RowsArgs{static_cast<const uint16_t *>(X) + m * x_stride, x_stride, r, K, q, k, scales}, st);
         if (e == hipSuccess)
             e = launch_int(IntArgs{q, W, scales, w_scales, static_cast<const uint16_t *>(bias),
-                                   static_cast<char *>(Y) + m * N * ysize, r, N, k, epilogue, out_dtype, rest, rest_bytes, v.cus},
+                                   static_cast<char *>(Y) + m * N * ysize, r, N, k, N, epilogue, out_dtype, rest, rest_bytes, v.cus,
+                                   v.counters, v.ncounters},
                            st);
         if (e != hipSuccess) return finish(ctx, e);
     }

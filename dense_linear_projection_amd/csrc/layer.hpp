@@ -21,12 +21,14 @@ struct IntArgs {
     const int8_t *X, *W;              // [M, K], [N, K]
     const float *x_scales, *w_scales; // [M], [N]
     const uint16_t *bias;             // bf16 [N] or nullptr
-    void *Y;                          // fp32 / bf16 [M, N]
-    int64_t M, N, K;
+    void *Y;                          // fp32 / bf16 [M, N], rows `row` elements apart
+    int64_t M, N, K, row;
     int epi, out;
     int32_t *ws;                      // sums of a split K
     size_t ws_bytes;
     int cus;
+    uint32_t *counters;               // ncounters of them, zero between calls
+    int ncounters;
 };
 // the largest K whose sum of products of 8-bit integers, each at most 2^14, stays below 2^31
 constexpr int64_t kIntMaxK = (int64_t{1} << 17) - 16;

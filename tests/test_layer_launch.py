@@ -84,8 +84,8 @@ int64_t stub_field(int i, const char *name) {
 }
 int stub_rows(int64_t M, int64_t K, int64_t stride) { return launch_quantize_rows(RowsArgs{nullptr, stride, M, K, nullptr, (K + 15) / 16 * 16, nullptr}, nullptr); }
 int stub_int(int64_t M, int64_t N, int64_t K, int64_t ws, int f32) {
-    return launch_int(IntArgs{nullptr, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<void *>(1 << 20), M, N, K, 0, f32 ? OUT_F32 : OUT_BF16,
-                              nullptr, static_cast<size_t>(ws), 256}, nullptr);
+    return launch_int(IntArgs{nullptr, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<void *>(1 << 20), M, N, K, N, 0, f32 ? OUT_F32 : OUT_BF16,
+                              nullptr, static_cast<size_t>(ws), 256, nullptr, 16384}, nullptr);
 }
 int stub_append(int64_t T, int q_heads, int heads, int dim, int rot) {
     AppendArgs a{};
