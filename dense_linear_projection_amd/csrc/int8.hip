@@ -6,6 +6,8 @@
 // The sum is exact (32-bit integers); it meets the scales in 64-bit floating
 // point, so that their product neither overflows nor vanishes on its way and
 // the result before bias and GELU is the rounded one.
+#include <type_traits>
+
 #include "layer.hpp"
 
 namespace proj {
@@ -263,6 +265,234 @@ __global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint3
     }
 }
 
+// Many tokens: bound by the matrix cores. One workgroup to a compute unit walks
+// BM x BN tiles; its eight waves (WM x WN of them over the tile, wave w and w + 4 on one
+// SIMD) are two groups that take turns: while one multiplies, the other reads its
+// fragments from LDS and issues its share of the copies. K goes in ranges of 128
+// bytes, whose halves (X rows, W rows) lie in a ring of five LDS slots filled by
+// global-to-LDS copies two ranges ahead; the ring runs on across tiles, so the next
+// tile's first ranges are on their way while this one is finished.
+//   * LDS rows are 128 bytes, the 16-byte chunk c of a row at position c ^ swizzle, so
+//     that the 16 rows of a fragment fall on different banks: for X bits 1..3 of the row,
+//     for W, whose fragments take rows 8 q + 4 j + t (q, t = 0..3) of a pair of blocks, bits
+//     1, 3 and 4. So a lane's results are eight consecutive outputs of one token.
+//   * group 0 reads step p of a range in one phase and multiplies in the next, group 1
+//     one phase later; a barrier stands between phases, and a range's copies are waited
+//     for just before the barrier that opens its first.
+__device__ __forceinline__ int swizzle_x(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swizzle_w(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
+
+// Barrier without a memory fence (the waits are explicit), which nothing moves across.
+__device__ __forceinline__ void barrier_only() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+template <int BM, int BN, int WM, int WN>
+struct IntTileCfg {
+    static constexpr int SLOTS = 5, SLOT = (BM > BN ? BM : BN) * 128;
+    static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+    static constexpr int NCA = BM / 64, NCB = BN / 64;  // copies of a wave in a range, each of eight rows
+    static constexpr int LDS = SLOTS * SLOT;
+    static constexpr int GROUP = 4;                     // tile rows that are walked together
+    static_assert(WM * WN == 8 && TM % 16 == 0 && TN % 32 == 0 && BM % 64 == 0 && BN % 64 == 0 && LDS <= 160 * 1024, "tile");
+};
+
+template <int BM, int BN, int WM, int WN, int OCC>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2 * OCC, 2 * OCC))) void int_tile_kernel(IntArgs a) {
+    using C = IntTileCfg<BM, BN, WM, WN>;
+    constexpr int FM = C::FM, FN = C::FN, SLOT = C::SLOT;
+    __shared__ __attribute__((aligned(16))) char lds[C::LDS];
+    const int tid = threadIdx.x, lane = tid & 63, fr = lane & 15, fg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), grp = wave >> 2, wg = wave & 3;
+    const int wm = wave / WN, wn = wave % WN;
+    const int K = static_cast<int>(a.K), KH = (K + 127) / 128;
+    const uint32_t tiles_m = static_cast<uint32_t>((a.M + BM - 1) / BM), tiles_n = static_cast<uint32_t>((a.N + BN - 1) / BN);
+    const uint32_t tiles = tiles_m * tiles_n;
+    // Tile of an item: ids go round the eight dies, whose items are neighbours, in groups of tile rows,
+    // so that operands are shared in a die's L2.
+    auto origin = [&](uint32_t item, int64_t &m0, int64_t &n0) {
+        const uint32_t at = tiles % 8 == 0 ? item % 8 * (tiles / 8) + item / 8 : item;
+        const uint32_t per = C::GROUP * tiles_n, gr = at / per, in = at - gr * per, first = gr * C::GROUP;
+        const uint32_t rows = tiles_m - first < C::GROUP ? tiles_m - first : C::GROUP;
+        const uint32_t ni = in / rows;
+        m0 = static_cast<int64_t>(first + in - ni * rows) * BM;
+        n0 = static_cast<int64_t>(ni) * BN;
+    };
+    auto resources = [&](uint32_t item, __amdgpu_buffer_rsrc_t &rx, __amdgpu_buffer_rsrc_t &rw) {
+        if (item >= tiles) {
+            rx = rw = buffer_rsrc(a.X, 0);
+            return;
+        }
+        int64_t m0, n0;
+        origin(item, m0, n0);
+        rx = buffer_rsrc(a.X + m0 * a.K, static_cast<uint32_t>((a.M - m0 < BM ? a.M - m0 : BM) * a.K));
+        rw = buffer_rsrc(a.W + n0 * a.K, static_cast<uint32_t>((a.N - n0 < BN ? a.N - n0 : BN) * a.K));
+    };
+    const int drow = lane >> 3;
+    uint32_t xoff[C::NCA], woff[C::NCB];
+#pragma unroll
+    for (int j = 0; j < C::NCA; ++j) {
+        const int row = (grp * (BM / 16) + wg + 4 * j) * 8 + drow;
+        xoff[j] = static_cast<uint32_t>(row * K + ((lane & 7) ^ swizzle_x(row)) * 16);
+    }
+#pragma unroll
+    for (int j = 0; j < C::NCB; ++j) {
+        const int row = (grp * (BN / 16) + wg + 4 * j) * 8 + drow;
+        woff[j] = static_cast<uint32_t>(row * K + ((lane & 7) ^ swizzle_w(row)) * 16);
+    }
+    auto copy_x = [&](__amdgpu_buffer_rsrc_t r, int T, int slot) {
+        if (T == KH - 1 && K % 128 != 0) {  // behind K lies the next row: zeros instead, here, so that W's do not matter
+#pragma unroll
+            for (int j = 0; j < C::NCA; ++j) {
+                const int row = (grp * (BM / 16) + wg + 4 * j) * 8 + drow;
+                const uint32_t v = T * 128 + ((lane & 7) ^ swizzle_x(row)) * 16 < K ? xoff[j] : kOutside;
+                dma16_buf(r, v, static_cast<uint32_t>(T * 128), lds + slot * SLOT + (grp * (BM / 16) + wg + 4 * j) * 1024);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < C::NCA; ++j)
+                dma16_buf(r, xoff[j], static_cast<uint32_t>(T * 128), lds + slot * SLOT + (grp * (BM / 16) + wg + 4 * j) * 1024);
+        }
+    };
+    auto copy_w = [&](__amdgpu_buffer_rsrc_t r, int T, int slot) {
+#pragma unroll
+        for (int j = 0; j < C::NCB; ++j)
+            dma16_buf(r, woff[j], static_cast<uint32_t>(T * 128), lds + slot * SLOT + (grp * (BN / 16) + wg + 4 * j) * 1024);
+    };
+    auto next = [](int slot, int d) { return slot + d >= C::SLOTS ? slot + d - C::SLOTS : slot + d; };
+    const int sx = swizzle_x(fr);  // the fragments' first rows are multiples of 16
+    auto frag_x = [&](const char *base, int i, int p) {
+        return *reinterpret_cast<const i32x4 *>(base + (wm * C::TM + i * 16 + fr) * 128 + (((4 * p + fg) ^ sx) << 4));
+    };
+    auto frag_w = [&](const char *base, int j, int p) {
+        const int row = wn * C::TN + (j >> 1) * 32 + 8 * (fr >> 2) + 4 * (j & 1) + (fr & 3);
+        return *reinterpret_cast<const i32x4 *>(base + row * 128 + (((4 * p + fg) ^ swizzle_w(row)) << 4));
+    };
+
+    uint32_t item = blockIdx.x;
+    __amdgpu_buffer_rsrc_t cx, cw, nx, nw;
+    resources(item, cx, cw);
+    int s0 = 0;  // slot of the current range's X; its W follows, then the next range's X
+    copy_x(cx, 0, 0);
+    copy_w(cw, 0, 1);
+    copy_x(cx, 1, 2);
+    resources(item + gridDim.x, nx, nw);
+    wait_vm<C::NCA>();
+    barrier_only();
+    for (; item < tiles; item += gridDim.x) {
+        i32x4 acc[FM][FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+        auto walk = [&](auto group) {
+            constexpr int GRP = decltype(group)::value;
+            if (GRP == 1) barrier_only();
+            i32x4 xf[FM], wf[FN];
+            for (int T = 0; T < KH; ++T) {
+                const char *xs = lds + s0 * SLOT, *ws = lds + next(s0, 1) * SLOT;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) xf[i] = frag_x(xs, i, p);
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) wf[j] = frag_w(ws, j, p);
+                    if (p == 0) {  // W of the next range, this tile's or the next tile's first
+                        if (T + 1 < KH)
+                            copy_w(cw, T + 1, next(s0, 3));
+                        else
+                            copy_w(nw, 0, next(s0, 3));
+                    } else {       // X of the one after that
+                        if (T + 2 < KH)
+                            copy_x(cx, T + 2, next(s0, 4));
+                        else
+                            copy_x(nx, T + 2 - KH, next(s0, 4));
+                    }
+                    if (GRP == 1 && p == 1) {
+                        wait_vm<C::NCA>();  // the next range has landed (this wave's part)
+                        lds_wait_all();     // the next phase refills the slot of X
+                    }
+                    barrier_only();
+                    lds_wait_all();
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < FM; ++i)
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) acc[i][j] = mfma16x16x64(wf[j], xf[i], acc[i][j]);
+                    if (GRP == 0 && p == 1) wait_vm<C::NCA>();
+                    barrier_only();
+                }
+                s0 = next(s0, 2);
+            }
+            if (GRP == 0) barrier_only();
+        };
+        if (grp == 0)
+            walk(std::integral_constant<int, 0>{});
+        else
+            walk(std::integral_constant<int, 1>{});
+
+        int64_t m0, n0;
+        origin(item, m0, n0);
+        m0 += wm * C::TM + fr;
+        n0 += wn * C::TN + 8 * fg;
+        // eight consecutive outputs of a token: acc[i][2 j][0 ..], acc[i][2 j + 1][0 ..]
+        const bool whole = a.row % 8 == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
+        float xs[FM];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) xs[i] = a.x_scales[m0 + 16 * i < a.M ? m0 + 16 * i : a.M - 1];
+#pragma unroll
+        for (int j = 0; j < FN / 2; ++j) {
+            const int64_t n = n0 + 32 * j;
+            float ws[8], bias[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t col = n + e < a.N ? n + e : a.N - 1;
+                ws[e] = a.w_scales[col];
+                bias[e] = (a.epi & 1) ? bf16_bits_to_f32(a.bias[col]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int64_t m = m0 + 16 * i;
+                if (m >= a.M || n >= a.N) continue;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] = scaled(acc[i][2 * j + e / 4][e % 4], xs[i], ws[e]);
+                    if (a.epi & 1) v[e] += bias[e];
+                    if (a.epi & 2) v[e] = gelu_tanh_fast(v[e]);
+                }
+                if (whole && n + 8 <= a.N && a.out == OUT_BF16) {
+                    u32x4 y;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = f32_to_bf16_bits(v[2 * e]) | static_cast<uint32_t>(f32_to_bf16_bits(v[2 * e + 1])) << 16;
+                    __builtin_nontemporal_store(y, reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.Y) + m * a.row + n));
+                } else if (whole && n + 8 <= a.N) {
+                    f32x4 *y = reinterpret_cast<f32x4 *>(static_cast<float *>(a.Y) + m * a.row + n);
+                    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, y);
+                    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, y + 1);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (n + e < a.N) store_out(a.Y, a.out, m * a.row + n + e, v[e]);
+                }
+            }
+        }
+        cx = nx;
+        cw = nw;
+        resources(item + 2 * gridDim.x, nx, nw);
+    }
+    wait_vm<0>();  // the copies for the tile after the last (empty resources) still write LDS
+}
+
+#define PROJ_INT_TILE_VARIANTS(X) X(256, 256, 4, 2, 1) X(256, 128, 4, 2, 1) X(128, 128, 4, 2, 2)
+#define PROJ_INT_TILE_INST(BM, BN, WM, WN, OCC) template __global__ void int_tile_kernel<BM, BN, WM, WN, OCC>(IntArgs);
+PROJ_INT_TILE_VARIANTS(PROJ_INT_TILE_INST)
+
 // K = 0: the sum is empty.
 __global__ __launch_bounds__(256) void int_empty_kernel(IntArgs a) {
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < a.M * a.N; i += static_cast<int64_t>(gridDim.x) * 256)
@@ -292,6 +522,14 @@ static hipError_t launch_int_stream(const IntArgs &a, hipStream_t st) {
     if (splits > static_cast<int64_t>(a.ws_bytes / (C::E * 4)) / tiles) splits = static_cast<int64_t>(a.ws_bytes / (C::E * 4)) / tiles;
     if (tiles > a.ncounters || splits < 1) splits = 1;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles * splits)), dim3(WAVES * 64), 0, st, a, static_cast<uint32_t>(splits));
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int OCC>
+static hipError_t launch_int_tile(const IntArgs &a, hipStream_t st) {
+    const int64_t tiles = (a.M + BM - 1) / BM * ((a.N + BN - 1) / BN), most = OCC * static_cast<int64_t>(a.cus);
+    hipLaunchKernelGGL((int_tile_kernel<BM, BN, WM, WN, OCC>), dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(512), 0,
+                       st, a);
     return hipGetLastError();
 }
 
@@ -328,7 +566,13 @@ hipError_t launch_int(const IntArgs &a, hipStream_t st) {
     if (a.M <= 16) return wide(2) ? launch_int_stream<1, 2, 4, 256, 9>(a, st) : launch_int_stream<1, 1, 4, 256, 9>(a, st);
     if (a.M <= 32) return launch_int_stream<2, 2, 4, 256, 9>(a, st);
     if (a.M <= 64) return wide(4) ? launch_int_stream<4, 4, 4, 256, 4>(a, st) : launch_int_stream<4, 2, 4, 256, 6>(a, st);
-    return wide(4) ? launch_int_stream<8, 4, 4, 256, 3>(a, st) : launch_int_stream<8, 2, 4, 256, 4>(a, st);
+    // tiles need two ranges of K at least, the ring looks that far ahead
+    if (a.K <= 128 || a.M <= 128)
+        return wide(4) ? launch_int_stream<8, 4, 4, 256, 3>(a, st) : launch_int_stream<8, 2, 4, 256, 4>(a, st);
+    auto tiles = [&](int bm, int bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
+    if (tiles(256, 256) > cus / 2) return launch_int_tile<256, 256, 4, 2, 1>(a, st);
+    if (tiles(256, 128) > cus / 2) return launch_int_tile<256, 128, 4, 2, 1>(a, st);
+    return launch_int_tile<128, 128, 4, 2, 2>(a, st);
 }
 #endif
 
