@@ -13,6 +13,7 @@
 namespace proj {
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
+typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------ rows to integers
@@ -32,11 +33,22 @@ struct RowScale {
         per = top == 0 || !numbers ? 0.f : 127.f / (most * up);
         scale = numbers ? most / 127.f : __builtin_nanf("");
     }
-    __device__ __forceinline__ uint32_t operator()(uint32_t bits) const {  // the integer's byte
-        const float y = __uint_as_float(bits << 16) * up * per;
-        const float z = __uint_as_float((__float_as_uint(y) + 16u) & ~31u);
-        // the integer nearest to z in the low bits; a NaN's place (its row's scale is NaN) is 0
-        return per == 0.f ? 0u : __float_as_uint(z + 0x1.8p23f) & 0xffu;
+    // eight elements' integers, in order. Where the row has no integers (zeros, or a NaN in it) they are 0.
+    __device__ __forceinline__ u32x2 operator()(u32x4 x) const {
+        uint32_t n[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float y = __uint_as_float(e % 2 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16) * up * per;
+            // 19 bits of y, and the nearest integer in the low bits of a number of 2^23
+            n[e] = __float_as_uint(__uint_as_float((__float_as_uint(y) + 16u) & ~31u) + 0x1.8p23f);
+        }
+        u32x2 q = {0u, 0u};
+        if (per != 0.f)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                q[h] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[4 * h + 3], n[4 * h + 2], 0x0c0c0400u),
+                                             __builtin_amdgcn_perm(n[4 * h + 1], n[4 * h], 0x0c0c0400u), 0x05040100u);
+        return q;
     }
 };
 
@@ -47,23 +59,66 @@ __device__ __forceinline__ u16x2 most8(u16x2 top, u32x4 w) {
     return top;
 }
 
-// One workgroup to a row, one element at a time.
-__global__ __launch_bounds__(256) void quantize_rows_kernel(RowsArgs a) {
+// Elements 8 c .. 8 c + 7 of a row, zeros behind its end.
+__device__ __forceinline__ u32x4 row_chunk(const uint16_t *x, int64_t c, int64_t K, bool vec) {
+    if (vec && 8 * c + 8 <= K) return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x + 8 * c));
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (8 * c < K)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (8 * c + e < K) w[e / 2] |= static_cast<uint32_t>(x[8 * c + e]) << (16 * (e % 2));
+    return w;
+}
+
+// LANES threads to a row, 256 to a workgroup. The row's R chunks of a thread stay in
+// registers between its largest element and its integers (R = 0: longer rows, read
+// twice). vec: rows start at 16-byte boundaries.
+template <int LANES, int R>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(RowsArgs a, int vec) {
+    constexpr int ROWS = 256 / LANES;
     __shared__ uint32_t peak[4];
-    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-        const uint16_t *x = a.X + m * a.stride;
-        uint32_t top = 0;
-        for (int64_t k = threadIdx.x; k < a.K; k += 256) top = max(top, static_cast<uint32_t>(x[k] & 0x7fff));
+    const int t = threadIdx.x % LANES;
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * ROWS; m0 < a.M; m0 += static_cast<int64_t>(gridDim.x) * ROWS) {
+        const int64_t m = m0 + threadIdx.x / LANES;
+        const bool there = m < a.M;
+        const uint16_t *x = a.X + (there ? m : a.M - 1) * a.stride;
+        u16x2 top2 = {0, 0};
+        u32x4 w[R > 0 ? R : 1];
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) w[r] = row_chunk(x, r * LANES + t, a.K, vec != 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) top2 = most8(top2, w[r]);
+        } else {
+            for (int64_t c = t; 8 * c < a.K; c += LANES) top2 = most8(top2, row_chunk(x, c, a.K, vec != 0));
+        }
+        uint32_t top = max(top2[0], top2[1]);
+#pragma unroll
         for (int h = 32; h >= 1; h >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), h, 64)));
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) peak[threadIdx.x >> 6] = top;
-        __syncthreads();
-        const RowScale s(max(max(peak[0], peak[1]), max(peak[2], peak[3])));
-        for (int64_t k = threadIdx.x; k < a.q_stride; k += 256)
-            a.q[m * a.q_stride + k] = static_cast<int8_t>(k < a.K ? s(x[k]) : 0u);
-        if (threadIdx.x == 0) a.scales[m] = s.scale;
+        if constexpr (LANES == 256) {
+            __syncthreads();  // the row before is done with
+            if ((threadIdx.x & 63) == 0) peak[threadIdx.x >> 6] = top;
+            __syncthreads();
+            top = max(max(peak[0], peak[1]), max(peak[2], peak[3]));
+        }
+        if (!there) continue;
+        const RowScale s(top);
+        int8_t *q = a.q + m * a.q_stride;
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (8 * (r * LANES + t) < a.q_stride) *reinterpret_cast<u32x2 *>(q + 8 * (r * LANES + t)) = s(w[r]);
+            for (int64_t c = R * LANES + t; 8 * c < a.q_stride; c += LANES) *reinterpret_cast<u32x2 *>(q + 8 * c) = u32x2{0u, 0u};
+        } else {
+            for (int64_t c = t; 8 * c < a.q_stride; c += LANES) *reinterpret_cast<u32x2 *>(q + 8 * c) = s(row_chunk(x, c, a.K, vec != 0));
+        }
+        if (t == 0) a.scales[m] = s.scale;
     }
 }
+
+#define PROJ_ROWS_VARIANTS(X) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(256, 4) X(256, 8) X(256, 0)
+#define PROJ_ROWS_INST(LANES, R) template __global__ void quantize_rows_kernel<LANES, R>(RowsArgs, int);
+PROJ_ROWS_VARIANTS(PROJ_ROWS_INST)
 
 // ------------------------------------------------------------------- product
 
@@ -505,10 +560,22 @@ __global__ __launch_bounds__(256) void int_empty_kernel(IntArgs a) {
 PROJ_INT_STREAM_VARIANTS(PROJ_INT_STREAM_INST)
 
 #ifndef __HIP_DEVICE_COMPILE__
-hipError_t launch_quantize_rows(const RowsArgs &a, hipStream_t st) {
-    const int64_t most = most_groups(256);
-    hipLaunchKernelGGL(quantize_rows_kernel, dim3(static_cast<unsigned>(a.M < most ? a.M : most)), dim3(256), 0, st, a);
+template <int LANES, int R>
+static hipError_t launch_rows(const RowsArgs &a, hipStream_t st) {
+    const int64_t groups = (a.M + 256 / LANES - 1) / (256 / LANES), most = most_groups(256);
+    const int vec = a.stride % 8 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0;
+    hipLaunchKernelGGL((quantize_rows_kernel<LANES, R>), dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(256), 0, st, a,
+                       vec);
     return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows(const RowsArgs &a, hipStream_t st) {
+    if (a.K <= 512) return launch_rows<64, 1>(a, st);
+    if (a.K <= 1024) return launch_rows<64, 2>(a, st);
+    if (a.K <= 2048) return launch_rows<256, 1>(a, st);
+    if (a.K <= 4096) return launch_rows<256, 2>(a, st);
+    if (a.K <= 8192) return launch_rows<256, 4>(a, st);
+    return a.K <= 16384 ? launch_rows<256, 8>(a, st) : launch_rows<256, 0>(a, st);
 }
 
 template <int MT, int NT, int WAVES, int KC, int D>
