@@ -10,16 +10,26 @@
 // sequence's length and window.
 //
 // A workgroup is four waves on (key-value head, part, group of rows), WQ of them
-// along the rows (32 to a wave) and 4 / WQ along the tokens. Tiles of keys and
-// values go through registers into LDS, in bf16 whatever the cache's type, those
-// of the next step on their way while this one is computed.
+// along the rows (32 to a wave) and 4 / WQ along the tokens. Keys and values go
+// into LDS in bf16 whatever the cache's type, those of the next step on their way
+// while this one is computed.
 //   * w: v_mfma_f32_32x32x16_bf16 with A = 32 tokens of K and B = 32 rows of q,
 //     held for the whole call. A lane of the result has row l % 32 and tokens
-//     8 (v / 4) + 4 (l / 32) + v % 4.
+//     8 (v / 4) + 4 (l / 32) + v % 4. The sums start at minus the row's running
+//     maximum, so what comes out is w - m without a subtraction.
 //   * o: A = V transposed (32 elements of the head x 16 tokens), B = the
 //     probabilities as they lie: slot 4 y + i of lane half h is token
 //     16 s + 8 y + 4 h + i of step s. V follows by being read in that order with
 //     LDS's transposing loads.
+//   * vector instructions and matrix ones take about the same time here, so the
+//     former are what counts. Logits stay in units of <q, k>, and the scale comes in
+//     the exponent; the maximum moves only when a logit passes it by more than 5
+//     (a factor of 148); the sign of the scale is put into q.
+//   * in LDS, tokens lie in sixteens, within those the 16-byte chunks of a token in
+//     fours: a lane copies chunks of one token only, whose address it works out
+//     once, and every read below has its place in its offset. Position
+//     (c % 4) ^ (token / 4 % 4) of a four holds chunk c: 16 tokens at one chunk, and
+//     four chunks of 4 tokens, fall on different banks.
 #include <type_traits>
 
 #include "layer.hpp"
@@ -31,7 +41,6 @@ typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 
 namespace {
 
-constexpr int kPages = 2048;  // tokens whose pages are staged at once
 constexpr float kLowest = -0x1.fffffep127f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -43,8 +52,6 @@ __device__ __forceinline__ u32x2 fp8x4_to_bf16(uint32_t w) {
     return r;
 }
 
-__device__ __forceinline__ float exp_above(float x, float most) { return __builtin_amdgcn_exp2f((x - most) * kLog2e); }
-
 // Two floats -> their bf16 halves, lo first: cut, or rounded to nearest even.
 __device__ __forceinline__ uint32_t cut2(float lo, float hi) {
     return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
@@ -55,36 +62,27 @@ __device__ __forceinline__ uint32_t round2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
-template <int D, bool FP8, int WQ>
+template <int D, int WQ>
 struct PrefixCfg {
-    static constexpr int WT = 4 / WQ;                       // waves along the tokens
-    static constexpr int SUB = WT == 1 ? 2 : 1;             // tiles of 32 tokens of a wave in a step
-    static constexpr int TOK = 32 * WT * SUB;               // tokens of a step
-    static constexpr int ROW = 2 * D;                       // bytes of a token in LDS
-    static constexpr int NC = ROW / 16;                     // its 16-byte chunks
-    static constexpr int UNITS = TOK * D * (FP8 ? 1 : 2) / 16;  // 16-byte loads of a step's keys (or values)
-    static constexpr int PER = (UNITS + 255) / 256;         // of them to a thread
-    static constexpr int UR = D * (FP8 ? 1 : 2) / 16;       // of them to a token
-    static constexpr int TILE = TOK * ROW;
-    static constexpr int BUFS = 4 * TILE <= (D <= 128 && WQ > 1 ? 80 : 152) * 1024 ? 2 : 1;
-    static constexpr int LDS = BUFS * 2 * TILE;
-    static constexpr int KS = D / 16, DT = (D + 31) / 32;
-    static constexpr int PERIOD = ROW % 256 == 0 ? 1 : ROW % 128 == 0 ? 2 : ROW % 64 == 0 ? 4 : 8;
-    // Where chunk c of row r lies, turned by the row. K: one chunk of 16 rows falls on different banks;
-    // V: four chunks of four rows do.
-    static __device__ __forceinline__ int place_k(int c, int r) { return (c + r / PERIOD) % NC; }
-    static __device__ __forceinline__ int place_v(int c, int r) { return (c + 4 * (r / PERIOD)) % NC; }
+    static constexpr int WT = 4 / WQ;                 // waves along the tokens
+    static constexpr int SUB = WT == 1 ? 2 : 1;       // tiles of 32 tokens of a wave in a step
+    static constexpr int TOK = 32 * WT * SUB;         // tokens of a step
+    static constexpr int U = TOK / 64;                // of them copied by a lane
+    static constexpr int NC = D / 8, CH = (NC + 3) / 4;  // 16-byte chunks of a token, fours of them
+    static constexpr int KS = D / 16, DT = CH;
+    static constexpr int TILE = TOK * CH * 64;        // bytes of a step's keys (or values)
+    static constexpr int UT = D / 16, UI = (UT + 3) / 4;  // 16-byte loads of a token in 8 bits, of a lane
+    static_assert(4 * TILE <= 128 * 1024, "two steps in LDS");
 };
 
 }  // namespace
 
 template <int D, bool FP8, int WQ, int TERMS>
-__global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel(PrefixArgs p) {
-    using C = PrefixCfg<D, FP8, WQ>;
+__global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kernel(PrefixArgs p) {
+    using C = PrefixCfg<D, WQ>;
     const AttendArgs &a = p.a;
-    __shared__ __attribute__((aligned(16))) char lds[C::LDS];
-    __shared__ uint32_t pages[kPages + 2];
-    __shared__ int bad;  // a page of the chunk is outside the cache
+    __shared__ __attribute__((aligned(16))) char lds[4 * C::TILE];
+    __shared__ int bad[3];  // a page of the step is outside the cache; by step % 3
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -98,6 +96,7 @@ __global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel
     const int h = static_cast<int>(pair / parts), part = static_cast<int>(pair % parts);
     const int per = a.q_heads / a.c.heads;
     const int64_t first = part * p.part, last = a.prefix < first + p.part ? a.prefix : first + p.part;
+    const int tokens = static_cast<int>(last - first), steps = (tokens + C::TOK - 1) / C::TOK;
 
     // this lane's row, and the tokens that it sees, counted from the part's first
     const int64_t rows = a.B * per, r = (static_cast<int64_t>(chunk) * WQ + wq) * 32 + c32;
@@ -110,134 +109,177 @@ __global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel
         hi = static_cast<int>((n < first ? first : n < last ? n : last) - first);
     }
     const bool none = hi <= lo;  // a row that sees nothing here: computed with the others, and dropped
+    // logits are to_logit <q, k>, q with the scale's sign (and zero, with the scale 1, for a scale of zero)
+    const float to_logit = a.scale == 0.f ? 1.f : fabsf(a.scale) * a.c.k_scale, c = to_logit * kLog2e, enough = 5.f / to_logit;
+    const uint32_t keep = a.scale == 0.f ? 0u : ~0u, flip = a.scale < 0.f ? 0x80008000u : 0u;
     bf16x8 q[C::KS];
 #pragma unroll
-    for (int i = 0; i < C::KS; ++i)
-        q[i] = load16(a.q + b * a.q_stride + (static_cast<int64_t>(h) * per + hq) * D + 16 * i + 8 * half);
-    f32x16 o[C::DT];
+    for (int i = 0; i < C::KS; ++i) {
+        u32x4 w = __builtin_bit_cast(u32x4, load16(a.q + b * a.q_stride + (static_cast<int64_t>(h) * per + hq) * D + 16 * i + 8 * half));
+        w = (w & keep) ^ flip;
+        q[i] = __builtin_bit_cast(bf16x8, w);
+    }
+    f32x16 o[C::DT], negm;  // negm: minus the running maximum, from which a sum starts
 #pragma unroll
-    for (int i = 0; i < C::DT; ++i)
+    for (int v = 0; v < 16; ++v) {
+        negm[v] = 0.f;
 #pragma unroll
-        for (int v = 0; v < 16; ++v) o[i][v] = 0.f;
-    float m = kLowest, l = 0.f;
+        for (int i = 0; i < C::DT; ++i) o[i][v] = 0.f;
+    }
+    // the maximum moves for a logit this far above it: any, before the first
+    float above = -__builtin_inff(), l = 0.f;
 
-    const char *kb = static_cast<const char *>(a.c.k) + h * a.c.kh * (FP8 ? 1 : 2);
-    const char *vb = static_cast<const char *>(a.c.v) + h * a.c.vh * (FP8 ? 1 : 2);
+    const int64_t kb_bytes = h * a.c.kh, vb_bytes = h * a.c.vh;
+    constexpr int SIZE = FP8 ? 1 : 2;
+    const char *kb = static_cast<const char *>(a.c.k) + kb_bytes * SIZE, *vb = static_cast<const char *>(a.c.v) + vb_bytes * SIZE;
     const int64_t place_mask = (int64_t{1} << a.c.page_shift) - 1;
-    const float to_logit = a.scale * a.c.k_scale;
-    u32x4 kr[C::PER], vr[C::PER];
+    u32x4 kr[C::U][C::UI], vr[C::U][C::UI];  // 8-bit keys and values on their way
+    int32_t page[C::U];                      // pages of the lane's tokens of the step that is copied next
 
-    for (int64_t base = first; base < last; base += kPages) {
-        const int64_t end = last < base + kPages ? last : base + kPages;
-        const int64_t page0 = base >> a.c.page_shift;
-        const int npages = static_cast<int>(((end - 1) >> a.c.page_shift) - page0) + 1;
-        const int left = static_cast<int>(end - base), in_page = static_cast<int>(base & place_mask);
-        const int steps = (left + C::TOK - 1) / C::TOK;
-        __syncthreads();  // the chunk before is done with
-        if (tid == 0) bad = 0;
-        __syncthreads();
-        for (int i = tid; i < npages; i += 256) {
-            const int32_t page = p.pages[page0 + i];
-            const bool ok = page >= 0 && page < a.c.pages;
-            pages[i] = ok ? static_cast<uint32_t>(page) : ~0u;
-            if (!ok) bad = 1;
+    // the lane's token of a step (behind the part's end: its last, masked later)
+    auto token = [&](int step, int u) -> int64_t {
+        const int t = step * C::TOK + (wave * C::U + u) * 16 + lane / 4;
+        return first + (t < tokens ? t : tokens - 1);
+    };
+    auto find_pages = [&](int step) {
+#pragma unroll
+        for (int u = 0; u < C::U; ++u) page[u] = p.pages[token(step, u) >> a.c.page_shift];
+    };
+    // Starts the copies of a step, whose pages are known; nothing is read through a wrong one.
+    auto copy = [&](int step, char *to) {
+#pragma unroll
+        for (int u = 0; u < C::U; ++u) {
+            const bool ok = page[u] >= 0 && page[u] < a.c.pages;
+            if (!ok) bad[step % 3] = 1;
+            const int64_t pg = ok ? page[u] : 0, place = token(step, u) & place_mask;
+            const char *ks = kb + (pg * a.c.kp + place * a.c.kt) * SIZE, *vs = vb + (pg * a.c.vp + place * a.c.vt) * SIZE;
+            if constexpr (FP8) {
+#pragma unroll
+                for (int i = 0; i < C::UI; ++i) {
+                    const int x = lane % 4 + 4 * i < C::UT ? lane % 4 + 4 * i : C::UT - 1;
+                    kr[u][i] = *reinterpret_cast<const u32x4 *>(ks + 16 * x);
+                    vr[u][i] = *reinterpret_cast<const u32x4 *>(vs + 16 * x);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::CH; ++i) {
+                    int x = 4 * i + ((lane % 4) ^ (lane >> 4));
+                    if (C::NC % 4 != 0 && x >= C::NC) x = C::NC - 1;
+                    dma16(ks + 16 * x, to + ((wave * C::U + u) * C::CH + i) * 1024);
+                    dma16(vs + 16 * x, to + C::TILE + ((wave * C::U + u) * C::CH + i) * 1024);
+                }
+            }
         }
+    };
+    // and ends them: 8-bit ones are widened on their way into LDS
+    auto land = [&](char *to) {
+        if constexpr (FP8) {
+#pragma unroll
+            for (int u = 0; u < C::U; ++u)
+#pragma unroll
+                for (int i = 0; i < C::UI; ++i)
+                    if (C::UT % 4 == 0 || lane % 4 + 4 * i < C::UT)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int ch = 2 * (lane % 4 + 4 * i) + e;
+                            char *at = to + ((wave * C::U + u) * C::CH + ch / 4) * 1024 + lane / 4 * 64 + ((ch % 4) ^ (lane >> 4)) * 16;
+                            const u32x2 k0 = fp8x4_to_bf16(kr[u][i][2 * e]), k1 = fp8x4_to_bf16(kr[u][i][2 * e + 1]);
+                            const u32x2 v0 = fp8x4_to_bf16(vr[u][i][2 * e]), v1 = fp8x4_to_bf16(vr[u][i][2 * e + 1]);
+                            *reinterpret_cast<u32x4 *>(at) = u32x4{k0[0], k0[1], k1[0], k1[1]};
+                            *reinterpret_cast<u32x4 *>(at + C::TILE) = u32x4{v0[0], v0[1], v1[0], v1[1]};
+                        }
+        } else {
+            wait_vm<0>();
+        }
+    };
+
+    // where this lane's pieces lie: chunk 2 i + half of token c32 (i even, i odd), and 4 elements of a V row for
+    // each of two rows eight apart
+    const int row0 = wt * C::SUB * 32;
+    int kat[2], vat[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        kat[x] = ((row0 + c32) / 16 * C::CH) * 1024 + c16 * 64 + (((2 * x + half) ^ (c16 / 4)) * 16);
+        const int row = 8 * x + 4 * half + c16 / 4, ch = 2 * ((lane >> 4) & 1) + (c16 & 3) / 2;
+        vat[x] = (row0 / 16 * C::CH) * 1024 + row * 64 + ((ch ^ (row / 4 % 4)) * 16) + (c16 & 1) * 8;
+    }
+
+    if (a.c.pages == 0) {  // no memory: whatever a row sees is outside the cache
+        above = none ? above : 0.f;
+        l = none ? 0.f : __builtin_nanf("");
+    } else if (steps > 0) {
+        if (tid < 3) bad[tid] = 0;
         __syncthreads();
-        const bool any_bad = bad != 0;
-
-        // the step's keys and values into registers; nothing is read through a wrong page
-        auto load = [&](int step) {
+        find_pages(0);
+        copy(0, lds);
+        if (steps > 1) find_pages(1);
+        land(lds);
+        __syncthreads();
+    }
+    for (int step = 0; step < steps && a.c.pages > 0; ++step) {
+        const char *kt = lds + (step & 1) * 2 * C::TILE, *vt = kt + C::TILE;
+        char *other = lds + ((step + 1) & 1) * 2 * C::TILE;
+        const bool any_bad = bad[step % 3] != 0;
+        if (tid == 0) bad[(step + 2) % 3] = 0;  // read a step ago, written in the next
+        if (step + 1 < steps) {
+            copy(step + 1, other);
+            if (step + 2 < steps) find_pages(step + 2);
+        }
+        const int t0 = step * C::TOK + row0;
+        if (!__all(hi <= t0 || lo >= t0 + 32 * C::SUB)) {  // a row of the wave sees some of it
+            f32x16 s[C::SUB];
 #pragma unroll
-            for (int i = 0; i < C::PER; ++i) {
-                const int id = i * 256 + tid < C::UNITS ? i * 256 + tid : C::UNITS - 1;
-                const int t = step * C::TOK + id / C::UR, at = in_page + (t < left ? t : left - 1);
-                const uint32_t page = pages[at >> a.c.page_shift];
-                const int64_t place = at & static_cast<int>(place_mask);
-                const int64_t ke = static_cast<int64_t>(page) * a.c.kp + place * a.c.kt;
-                const int64_t ve = static_cast<int64_t>(page) * a.c.vp + place * a.c.vt;
-                kr[i] = vr[i] = u32x4{0u, 0u, 0u, 0u};
-                if (page != ~0u) {
-                    kr[i] = *reinterpret_cast<const u32x4 *>(kb + (FP8 ? ke : 2 * ke) + id % C::UR * 16);
-                    vr[i] = *reinterpret_cast<const u32x4 *>(vb + (FP8 ? ve : 2 * ve) + id % C::UR * 16);
-                }
-            }
-        };
-        // and from there into LDS; values past the end are zero there: zero times NaN is not
-        auto store = [&](int step, char *kt, char *vt) {
-#pragma unroll
-            for (int i = 0; i < C::PER; ++i) {
-                const int id = i * 256 + tid, row = id / C::UR, u = id % C::UR;
-                if (C::UNITS % 256 != 0 && id >= C::UNITS) break;
-                if (step * C::TOK + row >= left) vr[i] = u32x4{0u, 0u, 0u, 0u};
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const u32x2 k0 = fp8x4_to_bf16(kr[i][2 * x]), k1 = fp8x4_to_bf16(kr[i][2 * x + 1]);
-                        const u32x2 v0 = fp8x4_to_bf16(vr[i][2 * x]), v1 = fp8x4_to_bf16(vr[i][2 * x + 1]);
-                        *reinterpret_cast<u32x4 *>(kt + row * C::ROW + C::place_k(2 * u + x, row) * 16) = u32x4{k0[0], k0[1], k1[0], k1[1]};
-                        *reinterpret_cast<u32x4 *>(vt + row * C::ROW + C::place_v(2 * u + x, row) * 16) = u32x4{v0[0], v0[1], v1[0], v1[1]};
-                    }
-                } else {
-                    *reinterpret_cast<u32x4 *>(kt + row * C::ROW + C::place_k(u, row) * 16) = kr[i];
-                    *reinterpret_cast<u32x4 *>(vt + row * C::ROW + C::place_v(u, row) * 16) = vr[i];
-                }
-            }
-        };
-
-        load(0);
-        for (int step = 0; step < steps; ++step) {
-            char *kt = lds + (step % C::BUFS) * 2 * C::TILE, *vt = kt + C::TILE;
-            if (C::BUFS == 1) __syncthreads();  // the step before is done with
-            store(step, kt, vt);
-            if (step + 1 < steps) load(step + 1);
-            __syncthreads();
-#pragma unroll
-            for (int sub = 0; sub < C::SUB; ++sub) {
-                const int row0 = (wt * C::SUB + sub) * 32;                         // the tile in LDS
-                const int t0 = static_cast<int>(base - first) + step * C::TOK + row0;  // and in the part
-                const int tiles_end = static_cast<int>(base - first) + left;
-                if (__all(hi <= t0 || lo >= t0 + 32)) continue;  // no row of the wave sees it
-                f32x16 s;
-#pragma unroll
-                for (int v = 0; v < 16; ++v) s[v] = 0.f;
+            for (int x = 0; x < C::SUB; ++x) {
+                s[x] = negm;
 #pragma unroll
                 for (int i = 0; i < C::KS; ++i) {
-                    const int row = row0 + c32;
-                    const bf16x8 k = *reinterpret_cast<const bf16x8 *>(kt + row * C::ROW + C::place_k(2 * i + half, row) * 16);
-                    s = mfma32x32x16(k, q[i], s);
+                    const bf16x8 k = *reinterpret_cast<const bf16x8 *>(kt + kat[i % 2] + x * 2 * C::CH * 1024 + i / 2 * 1024);
+                    s[x] = mfma32x32x16(k, q[i], s[x]);
                 }
-                float w[16], most = kLowest;
-                const bool whole = __all((lo <= t0 && hi >= t0 + 32) || none) && t0 + 32 <= tiles_end && !any_bad;
+            }
+            const bool whole = __all((lo <= t0 && hi >= t0 + 32 * C::SUB) || none) && t0 + 32 * C::SUB <= tokens && !any_bad;
+            if (!whole) {
 #pragma unroll
-                for (int v = 0; v < 16; ++v) w[v] = s[v] * to_logit;
-                if (!whole) {
+                for (int x = 0; x < C::SUB; ++x)
 #pragma unroll
                     for (int v = 0; v < 16; ++v) {
-                        const int t = t0 + 8 * (v / 4) + 4 * half + v % 4;
-                        if (t < lo || t >= hi || t >= tiles_end)
-                            w[v] = -__builtin_inff();
-                        else if (any_bad && pages[(in_page + t - static_cast<int>(base - first)) >> a.c.page_shift] == ~0u)
-                            w[v] = __builtin_nanf("");
+                        const int t = t0 + 32 * x + 8 * (v / 4) + 4 * half + v % 4;
+                        if (t < lo || t >= hi) {
+                            s[x][v] = -__builtin_inff();
+                        } else if (any_bad) {
+                            const int32_t pg = p.pages[(first + t) >> a.c.page_shift];
+                            if (pg < 0 || pg >= a.c.pages) s[x][v] = __builtin_nanf("");
+                        }
                     }
-                }
+            }
+            float most = s[0][0];
 #pragma unroll
-                for (int v = 0; v < 16; ++v) most = fmaxf(most, w[v]);
-                if (__any(most > m + 5.f)) {
-                    most = fmaxf(fmaxf(most, __shfl_xor(most, 32, 64)), m);
-                    const float f = exp_above(m, most);
-                    m = most;
-                    l *= f;
+            for (int x = 0; x < C::SUB; ++x)
 #pragma unroll
-                    for (int i = 0; i < C::DT; ++i) o[i] *= f;
-                }
+                for (int v = 0; v < 16; ++v) most = fmaxf(most, s[x][v]);
+            if (__any(most > above)) {
+                most = fmaxf(most, __shfl_xor(most, 32, 64));
+                const bool moves = most > above;
+                const float by = moves ? most : 0.f, f = above < 0.f ? 1.f : __builtin_amdgcn_exp2f(-by * c);
+                if (moves) above = enough;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < C::DT; ++i) o[i] *= f;
+                negm -= by;
+#pragma unroll
+                for (int x = 0; x < C::SUB; ++x) s[x] -= by;
+            }
+#pragma unroll
+            for (int x = 0; x < C::SUB; ++x) {
                 bf16x8 prob[TERMS][2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int y = 0; y < 2; ++y) {
                     uint32_t bits[TERMS][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float p0 = exp_above(w[8 * x + 2 * i], m), p1 = exp_above(w[8 * x + 2 * i + 1], m);
-                        l += p0 + p1;
+                        float p0 = __builtin_amdgcn_exp2f(s[x][8 * y + 2 * i] * c), p1 = __builtin_amdgcn_exp2f(s[x][8 * y + 2 * i + 1] * c);
+                        l += p0;
+                        l += p1;
 #pragma unroll
                         for (int k = 0; k < TERMS; ++k) {
                             if (k + 1 == TERMS) {
@@ -251,28 +293,28 @@ __global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel
                     }
 #pragma unroll
                     for (int k = 0; k < TERMS; ++k)
-                        prob[k][x] = __builtin_bit_cast(bf16x8, u32x4{bits[k][0], bits[k][1], bits[k][2], bits[k][3]});
+                        prob[k][y] = __builtin_bit_cast(bf16x8, u32x4{bits[k][0], bits[k][1], bits[k][2], bits[k][3]});
                 }
 #pragma unroll
                 for (int i = 0; i < C::DT; ++i)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        s16x4 y[2];
+                    for (int y = 0; y < 2; ++y) {
+                        s16x4 z[2];
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int row = row0 + 16 * x + 8 * j + 4 * half + c16 / 4;
-                            const int chunk_v = 4 * i + 2 * ((lane >> 4) & 1) + (c16 & 3) / 2;  // past the head: any other's
-                            y[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (__attribute__((address_space(3))) s16x4 *)(vt + row * C::ROW + C::place_v(chunk_v, row) * 16 + (c16 & 1) * 8));
-                        }
-                        const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                        for (int j = 0; j < 2; ++j)
+                            z[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (__attribute__((address_space(3))) s16x4 *)(vt + vat[j] + (2 * x + y) * C::CH * 1024 + i * 1024));
+                        const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(z[0], z[1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-                        for (int k = 0; k < TERMS; ++k) o[i] = mfma32x32x16(v, prob[k][x], o[i]);
+                        for (int k = 0; k < TERMS; ++k) o[i] = mfma32x32x16(v, prob[k][y], o[i]);
                     }
             }
         }
+        if (step + 1 < steps) land(other);
+        __syncthreads();
     }
     l += __shfl_xor(l, 32, 64);
+    const float top = -negm[0];
 
     // A sum that is not finite though its probabilities are: a value met a
     // probability of zero (a token that another row sees) or a vanished term.
@@ -295,10 +337,10 @@ __global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel
 #pragma unroll 1
         for (int64_t t = first; t < last; ++t) {
             const int at = static_cast<int>(t - first);
-            if (C::WT > 1 && at % kPages / 32 % C::WT != wt) continue;  // another wave's token
-            const int32_t page = p.pages[t >> a.c.page_shift];
-            if (page < 0 || page >= a.c.pages) continue;  // those that see it are NaN already
-            const int64_t ke = page * a.c.kp + (t & place_mask) * a.c.kt, ve = page * a.c.vp + (t & place_mask) * a.c.vt;
+            if (C::WT > 1 && at / 32 % C::WT != wt) continue;  // another wave's token
+            const int32_t pg = p.pages[t >> a.c.page_shift];
+            if (pg < 0 || pg >= a.c.pages) continue;  // those that see it are NaN already
+            const int64_t ke = pg * a.c.kp + (t & place_mask) * a.c.kt, ve = pg * a.c.vp + (t & place_mask) * a.c.vt;
             float dot = 0.f;
 #pragma unroll
             for (int i = 0; i < C::KS; ++i) {
@@ -312,7 +354,7 @@ __global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel
                 }
             }
             dot += __shfl_xor(dot, 32, 64);
-            const float prob = at >= lo && at < hi ? exp_above(dot * to_logit, m) : 0.f;
+            const float prob = at >= lo && at < hi ? __builtin_amdgcn_exp2f((dot - top) * c) : 0.f;
             if (!again || prob == 0.f) continue;
 #pragma unroll
             for (int i = 0; i < C::DT; ++i)
@@ -327,6 +369,7 @@ __global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel
         }
     }
 
+    float m = above < 0.f ? kLowest : top * to_logit;
     if (none) {
         m = kLowest;
         l = 0.f;
@@ -353,8 +396,8 @@ __global__ __launch_bounds__(256, D <= 128 && WQ > 1 ? 2 : 1) void prefix_kernel
     template __global__ void prefix_kernel<D, false, WQ, 3>(PrefixArgs); \
     template __global__ void prefix_kernel<D, true, WQ, 2>(PrefixArgs);  \
     template __global__ void prefix_kernel<D, true, WQ, 3>(PrefixArgs);
-#define PROJ_PREFIX_INST(D) \
-    PROJ_PREFIX_WQ(D, 1)    \
+#define PROJ_PREFIX_INST(D)               \
+    PROJ_PREFIX_WQ(D, (D <= 128 ? 1 : 2)) \
     PROJ_PREFIX_WQ(D, 4)
 PROJ_PREFIX_INST(64)
 PROJ_PREFIX_INST(80)
@@ -381,8 +424,10 @@ static hipError_t launch_shared_dim(PrefixArgs p, hipStream_t st) {
     const int64_t own_rows = a.B * a.c.heads * a.chunks, most = most_groups(256);
     // room for parts of a row: at least one of its own and one of the prefix
     const int64_t held = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
-    // the four waves along the tokens where one has all the rows (each then has a part of its own)
-    const int wq = rows <= 32 && held >= 5 ? 1 : 4, wt = 4 / wq;
+    // waves along the tokens where one has all the rows (each then has a part of its own): four, two where a step
+    // of four would not fit LDS
+    constexpr int kFew = D <= 128 ? 1 : 2;
+    const int wq = rows <= 32 && held > 4 / kFew ? kFew : 4, wt = 4 / wq;
     p.chunks = static_cast<int>((rows + 32 * wq - 1) / (32 * wq));
     if (held < 2 || own_rows > most - 7 * a.c.heads * a.chunks || a.B * a.q_heads > most ||
         (static_cast<int64_t>(a.c.heads) + 7) * p.chunks > most) {
@@ -408,7 +453,7 @@ static hipError_t launch_shared_dim(PrefixArgs p, hipStream_t st) {
         plan_attend(a, longest, room < most_parts ? room : most_parts);
     }
     const int64_t grid = (static_cast<int64_t>(a.c.heads) * parts + 7) / 8 * 8 * p.chunks;
-    hipError_t e = wq == 1 ? enqueue_prefix<D, 1>(p, grid, st) : enqueue_prefix<D, 4>(p, grid, st);
+    hipError_t e = wq == kFew ? enqueue_prefix<D, kFew>(p, grid, st) : enqueue_prefix<D, 4>(p, grid, st);
     if (e == hipSuccess && longest > 0) e = launch_attend_parts(a, st);
     return e != hipSuccess ? e : launch_attend_join(a, st);
 }
