@@ -58,7 +58,8 @@ struct AppendArgs {
     const void *q_norm = nullptr, *k_norm = nullptr;
     int norm_f32 = 0, norm_per_head = 0;
     float eps = 0.f;
-    int norm_lanes = 0;  // set by the launcher: lanes of a head
+    int norm_lanes = 0;  // set by the launcher: lanes of a head, and one over its size
+    float norm_share = 0.f;
 };
 hipError_t launch_append(const AppendArgs &a, hipStream_t st);
 

@@ -71,8 +71,9 @@ __device__ __forceinline__ void load8_weights(const AppendArgs &a, const void *n
 // NORM: a query or key head is first divided by the root of its mean square
 // (plus eps) and multiplied by its weights. A head's items are then neighbouring
 // lanes of one wave, 4, 8 or 16 of them (those past D / 16 have no elements), and
-// exchange their sums. Squares, their sum and the root are held in 64 bits: no
-// bf16 input overflows or vanishes there.
+// exchange their sums of squares, which are fp32 unless they near its ends: then
+// 64 bits, so that no bf16 input overflows or vanishes (64 bits for all heads took
+// 78 us where the plain append takes 62, their conversions at a quarter of the rate).
 template <int PAIRING, int TOK, bool NORM>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t blocks) {
     const int D = a.c.dim, per = NORM ? a.norm_lanes : D / 16;
@@ -115,23 +116,43 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t bloc
         pos[i] = a.positions[t0 + t];
         slot[i] = a.slots[t0 + t];
     }
+    float sum[TOK];  // of the head's squares
+    if (NORM && norm) {
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
+            sum[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum[i] = __builtin_fmaf(x[i][k / 8][k % 8], x[i][k / 8][k % 8], sum[i]);
+            if (idle) sum[i] = 0.f;
+        }
+        for (int h = 1; h < per; h <<= 1)
+#pragma unroll
+            for (int i = 0; i < TOK; ++i) sum[i] += __shfl_xor(sum[i], h, 64);
+    }
 #pragma unroll
     for (int i = 0; i < TOK; ++i) {
         if (t0 + i >= a.T) break;
         const bool known = a.rot == 0 || (pos[i] >= 0 && pos[i] < a.rope_rows);
         const float *cs = a.rope + static_cast<int64_t>(known ? pos[i] : 0) * a.rot;
-        double root = 1.0;  // 1 / sqrt(mean square + eps) of the head
+        float root = 1.f, up = 1.f;  // a normed element is x * up * root * weight
         if (NORM && norm) {
-            double sum = 0.0;
+            if (sum[i] > 0x1p-60f && sum[i] < 0x1p100f) {
+                root = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[i], a.norm_share, a.eps));
+            } else {  // squares, or their sum, near the ends of fp32 (or no numbers): in 64 bits
+                double wide = 0.0;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sum = __builtin_fma(x[i][k / 8][k % 8], static_cast<double>(x[i][k / 8][k % 8]), sum);
-            if (idle) sum = 0.0;
-            for (int h = 1; h < per; h <<= 1) sum += __shfl_xor(sum, h, 64);
-            const double mean = sum / D + static_cast<double>(a.eps);
-            root = 1.0 / sqrt(mean);
+                for (int k = 0; k < 16; ++k) wide = __builtin_fma(x[i][k / 8][k % 8], static_cast<double>(x[i][k / 8][k % 8]), wide);
+                if (idle) wide = 0.0;
+                for (int h = 1; h < per; h <<= 1) wide += __shfl_xor(wide, h, 64);
+                const double r = 1.0 / sqrt(wide / D + static_cast<double>(a.eps));
+                // up to 2^133 and down to 2^-128: brought near one by a power of two on either side
+                up = r > 0x1p60 ? 0x1p64f : r < 0x1p-60 ? 0x1p-64f : 1.f;
+                root = static_cast<float>(r / up);
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                x[i][k / 8][k % 8] = static_cast<float>(x[i][k / 8][k % 8] * root) * weight[k / 8][k % 8];
+                for (int k = 0; k < 16; ++k) x[i][k / 8][k % 8] *= up;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[i][k / 8][k % 8] = x[i][k / 8][k % 8] * root * weight[k / 8][k % 8];
         }
         if (turns && known) {
             if constexpr (PAIRING == kHalves) {
@@ -170,7 +191,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t bloc
                             const int partner = a.interleaved ? d ^ 1 : second ? d - half : d + half;
                             float u = bf16_bits_to_f32(row[i * a.stride + partner]);
                             if (NORM && norm)
-                                u = static_cast<float>(u * root) *
+                                u = u * up * root *
                                     (a.norm_f32 ? static_cast<const float *>(norm)[norm_at + partner]
                                                 : bf16_bits_to_f32(static_cast<const uint16_t *>(norm)[norm_at + partner]));
                             const float co = cs[j], si = cs[half + j];
@@ -210,8 +231,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t bloc
 #define PROJ_APPEND_INST(P)                                                    \
     template __global__ void append_kernel<P, 1, false>(AppendArgs, uint32_t); \
     template __global__ void append_kernel<P, 4, false>(AppendArgs, uint32_t); \
-    template __global__ void append_kernel<P, 1, true>(AppendArgs, uint32_t);  \
-    template __global__ void append_kernel<P, 4, true>(AppendArgs, uint32_t);
+    template __global__ void append_kernel<P, 1, true>(AppendArgs, uint32_t);
 PROJ_APPEND_INST(kHalves)
 PROJ_APPEND_INST(kNeighbours)
 PROJ_APPEND_INST(kAny)
@@ -220,11 +240,15 @@ PROJ_APPEND_INST(kAny)
 template <int PAIRING, bool NORM>
 static hipError_t launch_append_as(AppendArgs a, hipStream_t st) {
     a.norm_lanes = a.c.dim <= 64 ? 4 : a.c.dim <= 128 ? 8 : 16;
+    a.norm_share = 1.f / a.c.dim;
     const int64_t items = (static_cast<int64_t>(a.q_heads) + 2 * a.c.heads) * (NORM ? a.norm_lanes : a.c.dim / 16);
     const int64_t blocks = (items + 255) / 256;
-    // four tokens to a thread once that leaves enough threads for the chip
-    const int tok = a.T * items >= (int64_t{1} << 20) ? 4 : 1;
-    auto kernel = tok == 4 ? append_kernel<PAIRING, 4, NORM> : append_kernel<PAIRING, 1, NORM>;
+    // four tokens to a thread once that leaves enough threads for the chip; normed, one: the registers of four
+    // leave half as many waves (8192 tokens of 80 heads 74.5 us, with one 73.3)
+    const int tok = !NORM && a.T * items >= (int64_t{1} << 20) ? 4 : 1;
+    auto kernel = append_kernel<PAIRING, 1, NORM>;
+    if constexpr (!NORM)
+        if (tok == 4) kernel = append_kernel<PAIRING, 4, false>;
     // as many tokens at a time as one launch can have threads for
     const int64_t most = most_groups(256) / blocks * tok;
     AppendArgs s = a;

@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
     using C = PrefixCfg<D, WQ>;
     const AttendArgs &a = p.a;
     __shared__ __attribute__((aligned(16))) char lds[4 * C::TILE];
-    __shared__ int bad[3];  // a page of the step is outside the cache; by step % 3
+    __shared__ int bad[4];  // a page of the step is outside the cache; by step % 4
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -134,45 +134,45 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
     const char *kb = static_cast<const char *>(a.c.k) + kb_bytes * SIZE, *vb = static_cast<const char *>(a.c.v) + vb_bytes * SIZE;
     const int64_t place_mask = (int64_t{1} << a.c.page_shift) - 1;
     u32x4 kr[C::U][C::UI], vr[C::U][C::UI];  // 8-bit keys and values on their way
-    int32_t page[C::U];                      // pages of the lane's tokens of the step that is copied next
+    int32_t kpage[C::U], vpage[C::U];        // pages of the lane's tokens of the steps that are copied next
 
     // the lane's token of a step (behind the part's end: its last, masked later)
     auto token = [&](int step, int u) -> int64_t {
         const int t = step * C::TOK + (wave * C::U + u) * 16 + lane / 4;
         return first + (t < tokens ? t : tokens - 1);
     };
-    auto find_pages = [&](int step) {
+    auto find_pages = [&](int step, int32_t (&page)[C::U]) {
 #pragma unroll
         for (int u = 0; u < C::U; ++u) page[u] = p.pages[token(step, u) >> a.c.page_shift];
     };
-    // Starts the copies of a step, whose pages are known; nothing is read through a wrong one.
-    auto copy = [&](int step, char *to) {
+    // Starts the copies of a step's keys or values, whose pages are known; nothing is read through a wrong one.
+    auto copy = [&](int step, const int32_t (&page)[C::U], const char *from, int64_t page_stride, int64_t token_stride, char *to,
+                    u32x4 (&reg)[C::U][C::UI]) {
 #pragma unroll
         for (int u = 0; u < C::U; ++u) {
             const bool ok = page[u] >= 0 && page[u] < a.c.pages;
-            if (!ok) bad[step % 3] = 1;
-            const int64_t pg = ok ? page[u] : 0, place = token(step, u) & place_mask;
-            const char *ks = kb + (pg * a.c.kp + place * a.c.kt) * SIZE, *vs = vb + (pg * a.c.vp + place * a.c.vt) * SIZE;
+            if (!ok) bad[step % 4] = 1;
+            const char *at = from + ((ok ? page[u] : 0) * page_stride + (token(step, u) & place_mask) * token_stride) * SIZE;
             if constexpr (FP8) {
 #pragma unroll
                 for (int i = 0; i < C::UI; ++i) {
                     const int x = lane % 4 + 4 * i < C::UT ? lane % 4 + 4 * i : C::UT - 1;
-                    kr[u][i] = *reinterpret_cast<const u32x4 *>(ks + 16 * x);
-                    vr[u][i] = *reinterpret_cast<const u32x4 *>(vs + 16 * x);
+                    reg[u][i] = *reinterpret_cast<const u32x4 *>(at + 16 * x);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < C::CH; ++i) {
                     int x = 4 * i + ((lane % 4) ^ (lane >> 4));
                     if (C::NC % 4 != 0 && x >= C::NC) x = C::NC - 1;
-                    dma16(ks + 16 * x, to + ((wave * C::U + u) * C::CH + i) * 1024);
-                    dma16(vs + 16 * x, to + C::TILE + ((wave * C::U + u) * C::CH + i) * 1024);
+                    dma16(at + 16 * x, to + ((wave * C::U + u) * C::CH + i) * 1024);
                 }
             }
         }
     };
+    auto copy_k = [&](int step) { copy(step, kpage, kb, a.c.kp, a.c.kt, lds + (step & 1) * 2 * C::TILE, kr); };
+    auto copy_v = [&](int step) { copy(step, vpage, vb, a.c.vp, a.c.vt, lds + (step & 1) * 2 * C::TILE + C::TILE, vr); };
     // and ends them: 8-bit ones are widened on their way into LDS
-    auto land = [&](char *to) {
+    auto land = [&](const u32x4 (&reg)[C::U][C::UI], char *to) {
         if constexpr (FP8) {
 #pragma unroll
             for (int u = 0; u < C::U; ++u)
@@ -182,15 +182,19 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int ch = 2 * (lane % 4 + 4 * i) + e;
-                            char *at = to + ((wave * C::U + u) * C::CH + ch / 4) * 1024 + lane / 4 * 64 + ((ch % 4) ^ (lane >> 4)) * 16;
-                            const u32x2 k0 = fp8x4_to_bf16(kr[u][i][2 * e]), k1 = fp8x4_to_bf16(kr[u][i][2 * e + 1]);
-                            const u32x2 v0 = fp8x4_to_bf16(vr[u][i][2 * e]), v1 = fp8x4_to_bf16(vr[u][i][2 * e + 1]);
-                            *reinterpret_cast<u32x4 *>(at) = u32x4{k0[0], k0[1], k1[0], k1[1]};
-                            *reinterpret_cast<u32x4 *>(at + C::TILE) = u32x4{v0[0], v0[1], v1[0], v1[1]};
+                            const u32x2 w0 = fp8x4_to_bf16(reg[u][i][2 * e]), w1 = fp8x4_to_bf16(reg[u][i][2 * e + 1]);
+                            *reinterpret_cast<u32x4 *>(to + ((wave * C::U + u) * C::CH + ch / 4) * 1024 + lane / 4 * 64 +
+                                                       ((ch % 4) ^ (lane >> 4)) * 16) = u32x4{w0[0], w0[1], w1[0], w1[1]};
                         }
-        } else {
-            wait_vm<0>();
         }
+    };
+    auto land_k = [&](int step) { land(kr, lds + (step & 1) * 2 * C::TILE); };
+    auto land_v = [&](int step) { land(vr, lds + (step & 1) * 2 * C::TILE + C::TILE); };
+    // The page of step + 1's tokens serves its values now and served its keys a step ago.
+    auto next_pages = [&](int step) {
+#pragma unroll
+        for (int u = 0; u < C::U; ++u) vpage[u] = kpage[u];
+        if (step < steps) find_pages(step, kpage);
     };
 
     // where this lane's pieces lie: chunk 2 i + half of token c32 (i even, i odd), and 4 elements of a V row for
@@ -204,39 +208,50 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
         vat[x] = (row0 / 16 * C::CH) * 1024 + row * 64 + ((ch ^ (row / 4 % 4)) * 16) + (c16 & 1) * 8;
     }
 
+    // Sums of a step, started at minus the maximum.
+    f32x16 s[C::SUB];
+    auto multiply = [&](const char *kt) {
+#pragma unroll
+        for (int x = 0; x < C::SUB; ++x) {
+#pragma unroll
+            for (int i = 0; i < C::KS; ++i) {
+                const bf16x8 k = *reinterpret_cast<const bf16x8 *>(kt + kat[i % 2] + x * 2 * C::CH * 1024 + i / 2 * 1024);
+                s[x] = mfma32x32x16(k, q[i], i == 0 ? negm : s[x]);
+            }
+        }
+    };
+    const bool idle = __all(none);  // the wave only copies
     if (a.c.pages == 0) {  // no memory: whatever a row sees is outside the cache
         above = none ? above : 0.f;
         l = none ? 0.f : __builtin_nanf("");
     } else if (steps > 0) {
-        if (tid < 3) bad[tid] = 0;
+        if (tid < 4) bad[tid] = 0;
         __syncthreads();
-        find_pages(0);
-        copy(0, lds);
-        if (steps > 1) find_pages(1);
-        land(lds);
+        find_pages(0, kpage);
+        copy_k(0);
+        next_pages(1);
+        copy_v(0);
+        land_k(0);
+        if (steps > 1) copy_k(1);
+        next_pages(2);
+        land_v(0);
+        if (steps > 1) land_k(1);
+        wait_vm<0>();
         __syncthreads();
+        if (!idle) multiply(lds);
+        __syncthreads();  // the keys of the step after next go where these are
     }
+    // In a step: the copies of the next one's values and the keys of the one after it start, the sums become
+    // probabilities, and matrix operations follow all together, this step's values and the next one's keys: so one
+    // wave of a SIMD has its vector instructions while the other has these.
     for (int step = 0; step < steps && a.c.pages > 0; ++step) {
-        const char *kt = lds + (step & 1) * 2 * C::TILE, *vt = kt + C::TILE;
-        char *other = lds + ((step + 1) & 1) * 2 * C::TILE;
-        const bool any_bad = bad[step % 3] != 0;
-        if (tid == 0) bad[(step + 2) % 3] = 0;  // read a step ago, written in the next
-        if (step + 1 < steps) {
-            copy(step + 1, other);
-            if (step + 2 < steps) find_pages(step + 2);
-        }
+        const bool any_bad = bad[step % 4] != 0;
+        if (tid == 0) bad[(step + 3) % 4] = 0;  // read a step ago, written in the next
+        if (step + 1 < steps) copy_v(step + 1);
+        if (step + 2 < steps) copy_k(step + 2);
+        next_pages(step + 3);
         const int t0 = step * C::TOK + row0;
-        if (!__all(hi <= t0 || lo >= t0 + 32 * C::SUB)) {  // a row of the wave sees some of it
-            f32x16 s[C::SUB];
-#pragma unroll
-            for (int x = 0; x < C::SUB; ++x) {
-                s[x] = negm;
-#pragma unroll
-                for (int i = 0; i < C::KS; ++i) {
-                    const bf16x8 k = *reinterpret_cast<const bf16x8 *>(kt + kat[i % 2] + x * 2 * C::CH * 1024 + i / 2 * 1024);
-                    s[x] = mfma32x32x16(k, q[i], s[x]);
-                }
-            }
+        if (!idle) {
             const bool whole = __all((lo <= t0 && hi >= t0 + 32 * C::SUB) || none) && t0 + 32 * C::SUB <= tokens && !any_bad;
             if (!whole) {
 #pragma unroll
@@ -269,9 +284,9 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
 #pragma unroll
                 for (int x = 0; x < C::SUB; ++x) s[x] -= by;
             }
+            bf16x8 prob[C::SUB][TERMS][2];
 #pragma unroll
             for (int x = 0; x < C::SUB; ++x) {
-                bf16x8 prob[TERMS][2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     uint32_t bits[TERMS][4];
@@ -293,12 +308,17 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
                     }
 #pragma unroll
                     for (int k = 0; k < TERMS; ++k)
-                        prob[k][y] = __builtin_bit_cast(bf16x8, u32x4{bits[k][0], bits[k][1], bits[k][2], bits[k][3]});
+                        prob[x][k][y] = __builtin_bit_cast(bf16x8, u32x4{bits[k][0], bits[k][1], bits[k][2], bits[k][3]});
                 }
+            }
+            const char *vt = lds + (step & 1) * 2 * C::TILE + C::TILE;
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < C::DT; ++i)
+            for (int x = 0; x < C::SUB; ++x)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int i = 0; i < C::DT; ++i) {
                         s16x4 z[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
@@ -306,11 +326,25 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
                                 (__attribute__((address_space(3))) s16x4 *)(vt + vat[j] + (2 * x + y) * C::CH * 1024 + i * 1024));
                         const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(z[0], z[1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-                        for (int k = 0; k < TERMS; ++k) o[i] = mfma32x32x16(v, prob[k][y], o[i]);
+                        for (int k = 0; k < TERMS; ++k) o[i] = mfma32x32x16(v, prob[x][k][y], o[i]);
                     }
+            // the last step's are of no use, but a branch would part the matrix operations
+            multiply(lds + ((step + 1) & 1) * 2 * C::TILE);
+            // LDS reads eight ahead of the operations that need them
+            constexpr int READS = C::SUB * (4 * C::DT + C::KS), PRODUCTS = C::SUB * (2 * C::DT * TERMS + C::KS), AHEAD = 8;
+            __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+            for (int i = 0; i < READS - AHEAD; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
+            __builtin_amdgcn_sched_group_barrier(0x8, PRODUCTS - READS + AHEAD, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (step + 1 < steps) land(other);
+        // an 8-bit step's keys go where this step's were: every wave has multiplied those a step ago
+        if (step + 1 < steps) land_v(step + 1);
+        if (step + 2 < steps) land_k(step + 2);
+        wait_vm<0>();
         __syncthreads();
     }
     l += __shfl_xor(l, 32, 64);

@@ -395,8 +395,8 @@ proj_status proj_kv_append(proj_ctx *ctx, const proj_kv_cache *cache, const void
  * the query heads and k_norm for the key heads (NULL: those are not normed;
  * values never are), bf16 or fp32 (norm_dtype, a proj_out_dtype), 16-byte
  * aligned, [head_dim] for every head or, with norm_per_head, [q_heads][head_dim]
- * and [heads][head_dim]. The mean and the root are 64-bit, the result fp32 and
- * rounded where it is stored. eps is finite and not negative; with eps = 0 a head
+ * and [heads][head_dim]. Sums are fp32 (64-bit where squares near its ends), the
+ * result fp32 and rounded where it is stored. eps is finite and not negative; with eps = 0 a head
  * of zeros is NaN, as the formula is. A NaN in a head makes the head NaN. The
  * weights may not overlap q_out or the cache. */
 proj_status proj_kv_append_norm(proj_ctx *ctx, const proj_kv_cache *cache, const void *qkv, int64_t qkv_stride, int64_t T,

@@ -36,8 +36,10 @@ def product(X, x_scales, W, w_scales, bias, epilogue, out):
 
 
 def append_norm(k, v, qkv, q_norm, k_norm, eps, rope, positions, slots, q_heads, scales, interleaved):
-    """(q, k, v) in float64 and their tolerances; k and v [pages, heads, page, D] as stored values. A normed head is rounded
-    twice to fp32 (the quotient, its product with the weight); the rotation rounds two products and their sum."""
+    """(q, k, v) in float64 and their tolerances; k and v [pages, heads, page, D] as stored values. A normed element's roundings
+    to fp32, each 2^-24: the head's sum of squares, 16 added in a row and up to 4 such sums (20, halved by the root: 10), the
+    mean, two (1, halved), the root itself, good to a step (2), its product with x and that with the weight (2): 15. The
+    rotation rounds two products and their sum."""
     pages, heads, page, D = k.shape
     T, rot = qkv.shape[0], rope.shape[1]
     x = qkv.double().view(T, -1, D)
@@ -45,7 +47,7 @@ def append_norm(k, v, qkv, q_norm, k_norm, eps, rope, positions, slots, q_heads,
     for w, a, b in ((q_norm, 0, q_heads), (k_norm, q_heads, q_heads + heads)):
         if w is not None:
             y[:, a:b] = x[:, a:b] / torch.sqrt((x[:, a:b] ** 2).mean(-1, keepdim=True) + eps) * w.double()
-            e[:, a:b] = 2.001 * EPS32 * y[:, a:b].abs() + TINY
+            e[:, a:b] = 15 * EPS32 * y[:, a:b].abs() + TINY
     known = (positions >= 0) & (positions < rope.shape[0]) if rot else torch.ones(T, dtype=torch.bool)
     row = rope.double()[positions.long().clamp(0, max(0, rope.shape[0] - 1))] if rope.shape[0] else torch.zeros(T, rot).double()
     cos, sin = row[:, None, :rot // 2], row[:, None, rot // 2:]
