@@ -554,8 +554,10 @@ __global__ __launch_bounds__(256) void int_empty_kernel(IntArgs a) {
         store_out(a.Y, a.out, i, apply_epilogue(0.f, a.epi, (a.epi & 1) ? bf16_bits_to_f32(a.bias[i % a.N]) : 0.f));
 }
 
-#define PROJ_INT_STREAM_VARIANTS(X) \
-    X(1, 1, 4, 256, 9) X(1, 2, 4, 256, 9) X(2, 2, 4, 256, 9) X(4, 2, 4, 256, 6) X(4, 4, 4, 256, 4) X(8, 2, 4, 256, 4) X(8, 4, 4, 256, 3)
+#define PROJ_INT_STREAM_VARIANTS(X)                                                                       \
+    X(1, 1, 4, 256, 9) X(1, 2, 4, 256, 9) X(1, 4, 4, 256, 7) X(2, 2, 4, 256, 9) X(2, 4, 4, 256, 6)        \
+    X(4, 2, 4, 256, 6) X(4, 4, 4, 256, 4) X(4, 7, 4, 256, 3) X(6, 2, 4, 256, 5) X(6, 4, 4, 256, 3)        \
+    X(8, 2, 4, 256, 4) X(8, 4, 4, 256, 3)
 #define PROJ_INT_STREAM_INST(MT, NT, WV, KC, D) template __global__ void int_stream_kernel<MT, NT, WV, KC, D>(IntArgs, uint32_t);
 PROJ_INT_STREAM_VARIANTS(PROJ_INT_STREAM_INST)
 
@@ -578,17 +580,22 @@ hipError_t launch_quantize_rows(const RowsArgs &a, hipStream_t st) {
     return a.K <= 16384 ? launch_rows<256, 8>(a, st) : launch_rows<256, 0>(a, st);
 }
 
-template <int MT, int NT, int WAVES, int KC, int D>
-static hipError_t launch_int_stream(const IntArgs &a, hipStream_t st) {
-    using C = IntStreamCfg<MT, NT, WAVES, KC, D>;
-    auto kernel = int_stream_kernel<MT, NT, WAVES, KC, D>;
-    const int64_t tiles = (a.N + C::NR - 1) / C::NR * ((a.M + C::MR - 1) / C::MR), stages = (a.K + KC - 1) / KC;
-    // K is split while there are fewer tiles than compute units, in shares of four stages at least
+// How far K is split: while there are fewer tiles than compute units, in shares of four stages at least, as far as
+// the workspace holds the sums.
+static int64_t stream_splits(const IntArgs &a, int mt, int nt, int kc) {
+    const int64_t tiles = (a.N + 16 * nt - 1) / (16 * nt) * ((a.M + 16 * mt - 1) / (16 * mt)), stages = (a.K + kc - 1) / kc;
     int64_t splits = a.cus / tiles;
     if (splits > stages / 4) splits = stages / 4;
-    if (splits > static_cast<int64_t>(a.ws_bytes / (C::E * 4)) / tiles) splits = static_cast<int64_t>(a.ws_bytes / (C::E * 4)) / tiles;
-    if (tiles > a.ncounters || splits < 1) splits = 1;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tiles * splits)), dim3(WAVES * 64), 0, st, a, static_cast<uint32_t>(splits));
+    const int64_t room = static_cast<int64_t>(a.ws_bytes / (mt * nt * 1024)) / tiles;
+    if (splits > room) splits = room;
+    return tiles > a.ncounters || splits < 1 ? 1 : splits;
+}
+
+template <int MT, int NT, int WAVES, int KC, int D>
+static hipError_t launch_int_stream(const IntArgs &a, hipStream_t st) {
+    const int64_t tiles = (a.N + 16 * NT - 1) / (16 * NT) * ((a.M + 16 * MT - 1) / (16 * MT)), splits = stream_splits(a, MT, NT, KC);
+    hipLaunchKernelGGL((int_stream_kernel<MT, NT, WAVES, KC, D>), dim3(static_cast<unsigned>(tiles * splits)), dim3(WAVES * 64), 0, st, a,
+                       static_cast<uint32_t>(splits));
     return hipGetLastError();
 }
 
@@ -628,18 +635,34 @@ hipError_t launch_int(const IntArgs &a, hipStream_t st) {
         const hipError_t e = launch_int(x, st);
         return e != hipSuccess ? e : launch_int(y, st);
     }
+    // The kernel that is expected to be done first. Its time goes in rounds of one workgroup to a compute unit, each
+    // of a part that does not depend on K and one that does; in units of 0.15 us, K = 8192: streaming 40 and one for
+    // each row of X or W that a workgroup reads, a join of splits 10 and 4 for 256 outputs (M128 N8192 in 128 x 32 30 us,
+    // M64 N28672 in 64 x 112 48, M64 N8192 in 64 x 32 20.5, in two splits of 64 x 64 27.8), tiles 20
+    // and 380 (128 x 128; two of them to a unit 513), 420 (256 x 128), 540 (256 x 256) (M1024 N8192 in 256 x 128
+    // 70 us, the others 80 and 84; M512 N28672 in 256 x 256 117, the others 141 and 157).
+    const double deep = static_cast<double>(a.K) / 8192;
+    hipError_t (*best)(const IntArgs &, hipStream_t) = nullptr;
+    double least = 0;
+    auto offer = [&](double cost, hipError_t (*launch)(const IntArgs &, hipStream_t)) {
+        if (!best || cost < least) {
+            best = launch;
+            least = cost;
+        }
+    };
+    auto rounds = [&](int bm, int bn, int64_t units) { return ((a.M + bm - 1) / bm * ((a.N + bn - 1) / bn) + units - 1) / units; };
     const int64_t cus = a.cus;
-    auto wide = [&](int nt) { return (a.N + 16 * nt - 1) / (16 * nt) >= cus; };
-    if (a.M <= 16) return wide(2) ? launch_int_stream<1, 2, 4, 256, 9>(a, st) : launch_int_stream<1, 1, 4, 256, 9>(a, st);
-    if (a.M <= 32) return launch_int_stream<2, 2, 4, 256, 9>(a, st);
-    if (a.M <= 64) return wide(4) ? launch_int_stream<4, 4, 4, 256, 4>(a, st) : launch_int_stream<4, 2, 4, 256, 6>(a, st);
-    // tiles need two ranges of K at least, the ring looks that far ahead
-    if (a.K <= 128 || a.M <= 128)
-        return wide(4) ? launch_int_stream<8, 4, 4, 256, 3>(a, st) : launch_int_stream<8, 2, 4, 256, 4>(a, st);
-    auto tiles = [&](int bm, int bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
-    if (tiles(256, 256) > cus / 2) return launch_int_tile<256, 256, 4, 2, 1>(a, st);
-    if (tiles(256, 128) > cus / 2) return launch_int_tile<256, 128, 4, 2, 1>(a, st);
-    return launch_int_tile<128, 128, 4, 2, 2>(a, st);
+    if (a.K > 128) {  // tiles look two ranges of K ahead
+        const int64_t r = rounds(128, 128, cus);
+        offer(r == 1 ? 20 + 380 * deep : (r + 1) / 2 * (20 + 513 * deep), launch_int_tile<128, 128, 4, 2, 2>);
+        offer(rounds(256, 128, cus) * (20 + 420 * deep), launch_int_tile<256, 128, 4, 2, 1>);
+        offer(rounds(256, 256, cus) * (20 + 540 * deep), launch_int_tile<256, 256, 4, 2, 1>);
+    }
+#define PROJ_INT_STREAM_OFFER(MT, NT, WV, KC, D)                                                                  \
+    if (const int64_t r = rounds(16 * MT, 16 * NT, cus), s = stream_splits(a, MT, NT, KC); r * cus <= most - cus) \
+        offer(r * (40 + (s > 1 ? 10 + 4 * MT * NT : 0) + 16 * (MT + NT) * deep / s), launch_int_stream<MT, NT, WV, KC, D>);
+    PROJ_INT_STREAM_VARIANTS(PROJ_INT_STREAM_OFFER)
+    return best ? best(a, st) : hipErrorInvalidValue;
 }
 #endif
 
