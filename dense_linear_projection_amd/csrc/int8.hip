@@ -60,8 +60,10 @@ __device__ __forceinline__ u16x2 most8(u16x2 top, u32x4 w) {
 }
 
 // Elements 8 c .. 8 c + 7 of a row, zeros behind its end.
+template <bool ONCE = true>
 __device__ __forceinline__ u32x4 row_chunk(const uint16_t *x, int64_t c, int64_t K, bool vec) {
-    if (vec && 8 * c + 8 <= K) return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x + 8 * c));
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(x + 8 * c);
+    if (vec && 8 * c + 8 <= K) return ONCE ? __builtin_nontemporal_load(p) : *p;
     u32x4 w = {0u, 0u, 0u, 0u};
     if (8 * c < K)
 #pragma unroll
@@ -156,10 +158,17 @@ constexpr uint32_t kOutside = 0x80000000u;
 // fragment fall on different banks. W is read past the caches (non-temporal), X
 // stays in them. With S > 1 splits of K the last workgroup of a tile to
 // finish adds the others' sums, which lie in the workspace.
-template <int MT, int NT, int WAVES, int KC, int D>
+//
+// FUSED: very few tokens come as bf16 rows, and every workgroup makes them integers
+// itself, in LDS, while its first stages of W are on their way: their bytes are few
+// beside W's, and a launch less counts more (one token, K8192 N1024: 9.5 us a call
+// against 11.8).
+constexpr int kFusedRows = 4, kFusedK = 8192;  // rows whose chunks a workgroup's registers hold
+
+template <int MT, int NT, int WAVES, int KC, int D, bool FUSED = false>
 struct IntStreamCfg {
     static constexpr int NR = 16 * NT, MR = 16 * MT, CPR = KC / 16, RPI = 1024 / KC;
-    static constexpr int STAGE = (NR + MR) * KC;
+    static constexpr int STAGE = (NR + (FUSED ? 0 : MR)) * KC;
     static constexpr int PERW = STAGE / 1024 / WAVES;    // copies of a wave in a stage
     static constexpr int E = MT * NT * 256;              // outputs of a tile
     static constexpr int RED = WAVES * E * 4;
@@ -168,10 +177,13 @@ struct IntStreamCfg {
     static_assert(PERW * (D - 2) <= 63 && LDS <= 160 * 1024, "ring");
 };
 
-template <int MT, int NT, int WAVES, int KC, int D>
+template <int MT, int NT, int WAVES, int KC, int D, bool FUSED>
 __global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint32_t splits) {
-    using C = IntStreamCfg<MT, NT, WAVES, KC, D>;
+    using C = IntStreamCfg<MT, NT, WAVES, KC, D, FUSED>;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
+    __shared__ __attribute__((aligned(16))) char made[FUSED ? kFusedRows * kFusedK : 16];
+    __shared__ uint32_t peak[FUSED ? kFusedRows * WAVES : 1];
+    __shared__ float made_scale[FUSED ? kFusedRows : 1];
     const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t tiles_n = static_cast<uint32_t>((a.N + C::NR - 1) / C::NR);
@@ -195,8 +207,8 @@ __global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint3
 
     const int64_t rows_w = a.N - n0 < C::NR ? a.N - n0 : C::NR, rows_x = a.M - m0 < C::MR ? a.M - m0 : C::MR;
     const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(a.W + n0 * a.K, static_cast<uint32_t>(rows_w * a.K));
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X + m0 * a.K, static_cast<uint32_t>(rows_x * a.K));
-    const __amdgpu_buffer_rsrc_t none = buffer_rsrc(a.X, 0);
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.X + m0 * a.K, FUSED ? 0u : static_cast<uint32_t>(rows_x * a.K));
+    const __amdgpu_buffer_rsrc_t none = buffer_rsrc(a.W, 0);
     uint32_t voff[C::PERW];
     int chunk[C::PERW];
 #pragma unroll
@@ -227,8 +239,46 @@ __global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint3
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    constexpr int R = kFusedK / 8 / (WAVES * 64);
+    u32x4 row[FUSED ? kFusedRows : 1][R];  // asked for ahead of the copies: loads complete in order
+    if constexpr (FUSED) {
+        const bool vec = a.rows_stride % 8 == 0 && reinterpret_cast<uintptr_t>(a.rows) % 16 == 0;
+#pragma unroll
+        for (int m = 0; m < kFusedRows; ++m)
+            if (m < a.M)
+#pragma unroll
+                for (int r = 0; r < R; ++r) row[m][r] = row_chunk<false>(a.rows + m * a.rows_stride, r * WAVES * 64 + tid, a.rows_k, vec);
+    }
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) issue(i);
+    if constexpr (FUSED) {
+#pragma unroll
+        for (int m = 0; m < kFusedRows; ++m)
+            if (m < a.M) {
+                u16x2 top2 = {0, 0};
+#pragma unroll
+                for (int r = 0; r < R; ++r) top2 = most8(top2, row[m][r]);
+                uint32_t top = max(top2[0], top2[1]);
+#pragma unroll
+                for (int h = 32; h >= 1; h >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), h, 64)));
+                if (lane == 0) peak[m * WAVES + wave] = top;
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();  // the copies need not have landed
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int m = 0; m < kFusedRows; ++m)
+            if (m < a.M) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) top = max(top, peak[m * WAVES + w]);
+                const RowScale s(top);
+                if (tid == 0) made_scale[m] = s.scale;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (8 * (r * WAVES * 64 + tid) < K) *reinterpret_cast<u32x2 *>(made + m * K + 8 * (r * WAVES * 64 + tid)) = s(row[m][r]);
+            }
+    }
     for (int i = 0; i < nst; ++i) {
         wait_vm<C::PERW *(D - 2)>();  // this wave's copies of stage i have landed
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -240,8 +290,16 @@ __global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint3
         for (int s = 0; s < KC / 64 / WAVES; ++s) {
             const int c = (wave + s * WAVES) * 4 + g;
             i32x4 xf[MT], wf[NT];
+            if constexpr (FUSED) {
+                int stage = i + turn;
+                stage = (stage >= nst ? stage - nst : stage) + first;
+                const int k = stage * KC + 16 * c;
+                xf[0] = i32x4{0, 0, 0, 0};
+                if (c16 < rows_x && k < K) xf[0] = *reinterpret_cast<const i32x4 *>(made + c16 * K + k);
+            } else {
 #pragma unroll
-            for (int t = 0; t < MT; ++t) xf[t] = *reinterpret_cast<const i32x4 *>(slot + (C::NR + t * 16 + c16) * KC + ((c ^ c16) << 4));
+                for (int t = 0; t < MT; ++t) xf[t] = *reinterpret_cast<const i32x4 *>(slot + (C::NR + t * 16 + c16) * KC + ((c ^ c16) << 4));
+            }
 #pragma unroll
             for (int t = 0; t < NT; ++t) wf[t] = *reinterpret_cast<const i32x4 *>(slot + (t * 16 + c16) * KC + ((c ^ c16) << 4));
 #pragma unroll
@@ -316,7 +374,7 @@ __global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint3
         const int64_t m = m0 + t * 16 + ln % 16, n = n0 + u * 16 + 4 * (ln / 16);
         if (m >= a.M || n >= a.N) continue;
         const int32_t v[4] = {sum[q][0], sum[q][1], sum[q][2], sum[q][3]};
-        write4(a, m, n, v, a.x_scales[m]);
+        write4(a, m, n, v, FUSED ? made_scale[m] : a.x_scales[m]);
     }
 }
 
@@ -555,11 +613,13 @@ __global__ __launch_bounds__(256) void int_empty_kernel(IntArgs a) {
 }
 
 #define PROJ_INT_STREAM_VARIANTS(X)                                                                       \
-    X(1, 1, 4, 256, 9) X(1, 2, 4, 256, 9) X(1, 4, 4, 256, 7) X(2, 2, 4, 256, 9) X(2, 4, 4, 256, 6)        \
+    X(1, 1, 8, 512, 5) X(1, 2, 8, 512, 5) X(1, 4, 4, 256, 7) X(2, 2, 8, 512, 4) X(2, 4, 4, 256, 6)        \
     X(4, 2, 4, 256, 6) X(4, 4, 4, 256, 4) X(4, 7, 4, 256, 3) X(6, 2, 4, 256, 5) X(6, 4, 4, 256, 3)        \
     X(8, 2, 4, 256, 4) X(8, 4, 4, 256, 3)
-#define PROJ_INT_STREAM_INST(MT, NT, WV, KC, D) template __global__ void int_stream_kernel<MT, NT, WV, KC, D>(IntArgs, uint32_t);
+#define PROJ_INT_STREAM_INST(MT, NT, WV, KC, D) template __global__ void int_stream_kernel<MT, NT, WV, KC, D, false>(IntArgs, uint32_t);
 PROJ_INT_STREAM_VARIANTS(PROJ_INT_STREAM_INST)
+template __global__ void int_stream_kernel<1, 1, 8, 512, 5, true>(IntArgs, uint32_t);
+template __global__ void int_stream_kernel<1, 2, 8, 512, 5, true>(IntArgs, uint32_t);
 
 #ifndef __HIP_DEVICE_COMPILE__
 template <int LANES, int R>
@@ -580,21 +640,22 @@ hipError_t launch_quantize_rows(const RowsArgs &a, hipStream_t st) {
     return a.K <= 16384 ? launch_rows<256, 8>(a, st) : launch_rows<256, 0>(a, st);
 }
 
-// How far K is split: while there are fewer tiles than compute units, in shares of four stages at least, as far as
-// the workspace holds the sums.
-static int64_t stream_splits(const IntArgs &a, int mt, int nt, int kc) {
-    const int64_t tiles = (a.N + 16 * nt - 1) / (16 * nt) * ((a.M + 16 * mt - 1) / (16 * mt)), stages = (a.K + kc - 1) / kc;
+// How far K is split: while there are fewer tiles than compute units, in shares of 4096 at least (one token, K8192
+// N1024: two of them 7.4 us, four 7.7, one 7.5; 16 tokens, K16384 N512: 8.2, 9.3, 10.6), as far as the workspace
+// holds the sums.
+static int64_t stream_splits(const IntArgs &a, int mt, int nt) {
+    const int64_t tiles = (a.N + 16 * nt - 1) / (16 * nt) * ((a.M + 16 * mt - 1) / (16 * mt));
     int64_t splits = a.cus / tiles;
-    if (splits > stages / 4) splits = stages / 4;
+    if (splits > a.K / 4096) splits = a.K / 4096;
     const int64_t room = static_cast<int64_t>(a.ws_bytes / (mt * nt * 1024)) / tiles;
     if (splits > room) splits = room;
     return tiles > a.ncounters || splits < 1 ? 1 : splits;
 }
 
-template <int MT, int NT, int WAVES, int KC, int D>
+template <int MT, int NT, int WAVES, int KC, int D, bool FUSED = false>
 static hipError_t launch_int_stream(const IntArgs &a, hipStream_t st) {
-    const int64_t tiles = (a.N + 16 * NT - 1) / (16 * NT) * ((a.M + 16 * MT - 1) / (16 * MT)), splits = stream_splits(a, MT, NT, KC);
-    hipLaunchKernelGGL((int_stream_kernel<MT, NT, WAVES, KC, D>), dim3(static_cast<unsigned>(tiles * splits)), dim3(WAVES * 64), 0, st, a,
+    const int64_t tiles = (a.N + 16 * NT - 1) / (16 * NT) * ((a.M + 16 * MT - 1) / (16 * MT)), splits = stream_splits(a, MT, NT);
+    hipLaunchKernelGGL((int_stream_kernel<MT, NT, WAVES, KC, D, FUSED>), dim3(static_cast<unsigned>(tiles * splits)), dim3(WAVES * 64), 0, st, a,
                        static_cast<uint32_t>(splits));
     return hipGetLastError();
 }
@@ -605,6 +666,14 @@ static hipError_t launch_int_tile(const IntArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((int_tile_kernel<BM, BN, WM, WN, OCC>), dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(512), 0,
                        st, a);
     return hipGetLastError();
+}
+
+bool int_fuses(int64_t M, int64_t N, int64_t K) {
+    return K > 0 && M <= kFusedRows && K <= kFusedK && (N + 15) / 16 <= most_groups(256);
+}
+
+hipError_t launch_int_fused(const IntArgs &a, hipStream_t st) {
+    return (a.N + 31) / 32 >= a.cus ? launch_int_stream<1, 2, 8, 512, 5, true>(a, st) : launch_int_stream<1, 1, 8, 512, 5, true>(a, st);
 }
 
 hipError_t launch_int(const IntArgs &a, hipStream_t st) {
@@ -659,7 +728,7 @@ hipError_t launch_int(const IntArgs &a, hipStream_t st) {
         offer(rounds(256, 256, cus) * (20 + 540 * deep), launch_int_tile<256, 256, 4, 2, 1>);
     }
 #define PROJ_INT_STREAM_OFFER(MT, NT, WV, KC, D)                                                                  \
-    if (const int64_t r = rounds(16 * MT, 16 * NT, cus), s = stream_splits(a, MT, NT, KC); r * cus <= most - cus) \
+    if (const int64_t r = rounds(16 * MT, 16 * NT, cus), s = stream_splits(a, MT, NT); r * cus <= most - cus) \
         offer(r * (40 + (s > 1 ? 10 + 4 * MT * NT : 0) + 16 * (MT + NT) * deep / s), launch_int_stream<MT, NT, WV, KC, D>);
     PROJ_INT_STREAM_VARIANTS(PROJ_INT_STREAM_OFFER)
     return best ? best(a, st) : hipErrorInvalidValue;

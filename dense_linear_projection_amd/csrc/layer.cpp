@@ -128,6 +128,14 @@ proj_status proj_run_int_dynamic(proj_ctx *ctx, const void *X, int64_t x_stride,
     if (rows > M) rows = M;
     DeviceGuard g(v.device);
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (int_fuses(M, N, k)) {
+        IntArgs a{nullptr, W, nullptr, w_scales, static_cast<const uint16_t *>(bias), Y, M, N, k, N, epilogue,
+                  out_dtype, reinterpret_cast<int32_t *>(v.ws), v.ws_bytes, v.cus, v.counters, v.ncounters};
+        a.rows = static_cast<const uint16_t *>(X);
+        a.rows_stride = x_stride;
+        a.rows_k = K;
+        return finish(ctx, launch_int_fused(a, st));
+    }
     float *scales = v.ws;
     const int64_t sb = (rows * 4 + 255) / 256 * 256, qb = (rows * k + 255) / 256 * 256;
     int8_t *q = reinterpret_cast<int8_t *>(v.ws) + sb;

@@ -29,10 +29,15 @@ struct IntArgs {
     int cus;
     uint32_t *counters;               // ncounters of them, zero between calls
     int ncounters;
+    const uint16_t *rows = nullptr;   // fused: the tokens in bf16 [M, rows_k], rows_stride elements apart, instead of X
+    int64_t rows_stride = 0, rows_k = 0;
 };
 // the largest K whose sum of products of 8-bit integers, each at most 2^14, stays below 2^31
 constexpr int64_t kIntMaxK = (int64_t{1} << 17) - 16;
 hipError_t launch_int(const IntArgs &a, hipStream_t st);
+// Whether the product takes so few tokens (K rounded up) in bf16, and that product: `rows` instead of X and x_scales.
+bool int_fuses(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int_fused(const IntArgs &a, hipStream_t st);
 
 // Attention of one new token for each sequence behind a shared prefix: `a` with
 // a.prefix tokens in the pages of `pages`. hipErrorOutOfMemory (and nothing

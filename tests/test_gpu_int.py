@@ -164,11 +164,12 @@ def test_every_split_gives_the_same_bits():
 
 # ------------------------------------------------------------- from bf16 tokens
 
-@pytest.mark.parametrize("M,N,K", [(1, 100, 1000), (7, 515, 1000), (16, 512, 2048), (33, 64, 33), (300, 515, 1000), (1200, 600, 520),
+@pytest.mark.parametrize("M,N,K", [(1, 100, 1000), (1, 1, 8), (1, 8200, 32768), (1, 300, 32769), (2, 515, 8192), (3, 40, 2049), (4, 8192, 8192),
+                                   (4, 17, 100), (4, 64, 8193), (5, 64, 2048), (7, 515, 1000), (16, 512, 2048), (33, 64, 33), (300, 515, 1000), (1200, 600, 520),
                                    (5, 40, 1), (64, 1024, 4096)])
 def test_dynamic_is_the_two_calls(ctx, M, N, K):
     g = torch.Generator().manual_seed(K)
-    X = torch.randn(M, K + 8, generator=g).to(BF16).cuda()[:, :K]
+    X = torch.randn(M, K + 8, generator=g).to(BF16).cuda()[:, N % 3:K + N % 3]
     W, ws = dlp.proj_quantize_rows(ctx, torch.randn(N, K, generator=g).to(BF16).cuda())
     bias = torch.randn(N, generator=g).to(BF16).cuda()
     for epi, out in ((0, F32), (3, BF16)):

@@ -26,6 +26,7 @@ static IntArgs products[64];
 static int nrows, nproducts;
 static AppendArgs appended;
 static PrefixArgs shared;
+static IntArgs fused;
 extern "C" int stub_launches() { return launches; }
 extern "C" const char *stub_message() { return message; }
 extern "C" void stub_room(int64_t n) { room = n; nrows = nproducts = 0; }
@@ -46,6 +47,7 @@ extern "C" int64_t stub_piece(int i, int what) {
     }
     return -1;
 }
+extern "C" int stub_fused(int64_t X) { return fused.rows == reinterpret_cast<uint16_t *>(X) && fused.rows_stride == 300 && fused.rows_k == 251 && fused.K == 256; }
 extern "C" int64_t stub_prefix() { return shared.a.prefix; }
 extern "C" int stub_norm() { return (appended.q_norm ? 1 : 0) | (appended.k_norm ? 2 : 0) | appended.norm_f32 * 4 | appended.norm_per_head * 8; }
 namespace proj {
@@ -63,6 +65,8 @@ proj_status context_error(proj_ctx *, proj_status s, const char *fmt, ...) {
 }
 hipError_t launch_quantize_rows(const RowsArgs &a, hipStream_t) { ++launches; if (nrows < 64) rows[nrows++] = a; return hipSuccess; }
 hipError_t launch_int(const IntArgs &a, hipStream_t) { ++launches; if (nproducts < 64) products[nproducts++] = a; return hipSuccess; }
+bool int_fuses(int64_t M, int64_t, int64_t) { return M == 99; }
+hipError_t launch_int_fused(const IntArgs &a, hipStream_t) { fused = a; ++launches; return hipSuccess; }
 hipError_t launch_append(const AppendArgs &a, hipStream_t) { appended = a; ++launches; return hipSuccess; }
 hipError_t launch_attend(const AttendArgs &a, hipStream_t) { shared = PrefixArgs{}; shared.a = a; ++launches; return hipSuccess; }
 hipError_t launch_attend_shared(const PrefixArgs &p, hipStream_t) {
@@ -157,6 +161,8 @@ def test_run_int_dynamic(host):
     host.stub_room(64 << 20)
     case(OK, 2)
     case(OK, 2, K=251)
+    case(OK, 1, M=99, K=251)
+    assert host.stub_fused(ctypes.c_int64(A))
     case(OK, 2, X=A + 2)
     case(OK, 2, K=0, X=None, W=None, ws=None)
     case(OK, M=0, X=None)
