@@ -473,10 +473,10 @@ static hipError_t launch_shared_dim(PrefixArgs p, hipStream_t st) {
         x.a = attend_rest(a, x.a.B);
         return launch_shared_dim<D>(x, st);
     }
-    // parts of the prefix: two workgroups to a compute unit, none shorter than 256 tokens
+    // parts of the prefix: two workgroups to a compute unit, none shorter than 128 tokens
     const int64_t pairs = static_cast<int64_t>(a.c.heads) * p.chunks;
     int64_t parts = (2 * static_cast<int64_t>(a.cus) + pairs - 1) / pairs;
-    if (parts > (a.prefix + 255) / 256) parts = (a.prefix + 255) / 256;
+    if (parts > (a.prefix + 127) / 128) parts = (a.prefix + 127) / 128;
     if (parts > (held - 1) / wt) parts = (held - 1) / wt;
     if (parts < 1) parts = 1;
     p.part = ((a.prefix + parts - 1) / parts + 127) / 128 * 128;
