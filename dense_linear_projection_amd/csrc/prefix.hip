@@ -30,6 +30,12 @@
 //     once, and every read below has its place in its offset. Position
 //     (c % 4) ^ (token / 4 % 4) of a four holds chunk c: 16 tokens at one chunk, and
 //     four chunks of 4 tokens, fall on different banks.
+//   * a probability enters as bf16 terms, two for bf16 results (16 of its bits: errors
+//     against 64 bits as with all 24; with one term, 12% faster for 256 sequences, they
+//     are 1.4 times as large) and three for fp32 ones.
+// 256 sequences of 64 query heads behind 32768 tokens (8 heads of 128, bf16) 375 to 436 us
+// for the prefix, 0.63 to 0.73e15 operations a second of the formula's; the matrix cores
+// work in half of the cycles, vector instructions issue in the other half.
 #include <type_traits>
 
 #include "layer.hpp"

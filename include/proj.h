@@ -42,7 +42,7 @@
  *
  * Memory the library owns: per context, the split-K workspace (exactly the
  * caller's bound, given to proj_create), 1.25 KiB of zero page and sink and
- * 64 KiB of counters (proj_kv_attend);
+ * 64 KiB of counters (proj_kv_attend, proj_run_int);
  * per tuning call, the flush buffer and operand copies above; per GPU, the 2 MiB static array
  * of split-K partials that proj_run_noalloc uses (part of the library's code
  * object, held until the process ends).  Nothing else.

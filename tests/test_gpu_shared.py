@@ -271,6 +271,31 @@ def test_spread_of_logits(ctx):
             close(lse, want[1], tol[1])
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1e-30, -1e-42, 2.0, -30.0])
+def test_scales(ctx, scale):
+    """Scales of either sign, zero, so small that every token counts alike, so large that one does."""
+    for B, Hq in ((3, 8), (40, 8)):
+        lengths = lengths_of(B, 150, 60, B)
+        lengths[0] = 33
+        k, v, cache, q, prefix, tables, n, _ = make(B, Hq, 2, 64, 16, BF16, "hnd", 150, lengths, 18)
+        want, tol = ref.attend_shared(k, v, q, prefix, 150, tables, n, scale, 0, (1, 1), F32)
+        o, lse = run(ctx, cache, q, prefix, 150, tables, n, scale, F32)
+        close(o, want[0], tol[0])
+        close(lse, want[1], tol[1])
+
+
+def test_queries_that_are_not_numbers(ctx):
+    k, v, cache, q, prefix, tables, n, _ = make(40, 8, 2, 64, 16, BF16, "hnd", 150, [170] * 40, 19)
+    want, tol = ref.attend_shared(k, v, q, prefix, 150, tables, n, 0.1, 0, (1, 1), F32)
+    q[7, 3, 5], q[9, 0] = float("nan"), float("inf")
+    o, lse = run(ctx, cache, q, prefix, 150, tables, n, 0.1, F32)
+    keep = torch.ones(40, 8, dtype=torch.bool)
+    keep[7, 3] = keep[9, 0] = False
+    assert torch.isnan(o[7, 3]).all() and torch.isnan(lse[7, 3])
+    close(o[keep], want[0][keep], tol[0][keep])
+    close(lse[keep], want[1][keep], tol[1][keep])
+
+
 def test_workspaces():
     """Whatever the workspace holds, the result is right: fewer parts, fewer sequences at a time, a refusal at last."""
     B, Hq, H, D, L = 30, 16, 2, 64, 600
