@@ -112,3 +112,39 @@ def test_layer(ctx, B, fp8):
         # results before them differ: one step of either in a few of a row's elements, of 512 that add up at random.
         off = (y.cpu().double() - want).norm() / want.norm()
         assert float(off) < 2.0 ** -7, (t, float(off))
+
+
+def test_two_contexts_at_once():
+    """Two contexts on two streams, whose kernels overlap: splits of K, joins and partial results do not meet."""
+    g = torch.Generator().manual_seed(7)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    contexts = [dlp.proj_create(0) for _ in range(2)]
+    calls = []
+    for i in range(2):
+        X = torch.randn(16, 8192, generator=g).to(BF16).cuda()
+        W = dlp.proj_quantize_rows(contexts[0], torch.randn(512, 8192, generator=g).to(BF16).cuda())
+        k, v = (torch.randn(40, 2, 16, 64, generator=g).to(BF16).cuda() for _ in range(2))
+        q, order = torch.randn(24, 8, 64, generator=g).to(BF16).cuda(), torch.randperm(40, generator=g).int().cuda()
+        n = torch.randint(100, 117, (24,), generator=g).int().cuda()
+        calls.append((X, W, dlp.kv_cache(k, v), q, order[:7].contiguous(), order[7:31].view(24, 1), n))
+
+    def run(ctx, c, stream):
+        X, W, cache, q, prefix, tables, n = c
+        with torch.cuda.stream(stream):
+            Y, o, lse = torch.empty(16, 512, device="cuda"), torch.empty(24, 8, 64, device="cuda"), torch.empty(24, 8, device="cuda")
+            for _ in range(5):
+                dlp.proj_run_int_dynamic(ctx, X, *W, None, dlp.EPI_NONE, Y)
+                dlp.proj_kv_attend_shared(ctx, cache, q, prefix, 100, tables, n, 0.1, o, lse=lse)
+        return Y, o, lse
+
+    torch.cuda.synchronize()
+    alone = []
+    for i in range(2):
+        alone.append(run(contexts[i], calls[i], sides[i]))
+        torch.cuda.synchronize()
+    both = [run(contexts[i], calls[i], sides[i]) for _ in range(4) for i in range(2)]
+    torch.cuda.synchronize()
+    for j, got in enumerate(both):
+        assert all(torch.equal(a, b) for a, b in zip(got, alone[j % 2]))
+    for c in contexts:
+        dlp.proj_destroy(c)
