@@ -9,10 +9,11 @@
 // (attend.hip). A row sees the tokens lo <= t < hi of the prefix, by its
 // sequence's length and window.
 //
-// A workgroup is four waves on (key-value head, part, group of rows), WQ of them
-// along the rows (32 to a wave) and 4 / WQ along the tokens. Keys and values go
-// into LDS in bf16 whatever the cache's type, those of the next step on their way
-// while this one is computed.
+// A workgroup is four waves on (key-value head, part, group of 128 rows), 32 rows to
+// a wave. Keys and values go into LDS in bf16 whatever the cache's type, 64 tokens
+// to a step, those of the next steps on their way while this one is computed. Waves
+// without rows only copy: with 32 rows in all, four waves on different tokens, each
+// with a part of its own, took 78 us for 65536 tokens where these take 58.
 //   * w: v_mfma_f32_32x32x16_bf16 with A = 32 tokens of K and B = 32 rows of q,
 //     held for the whole call. A lane of the result has row l % 32 and tokens
 //     8 (v / 4) + 4 (l / 32) + v % 4. The sums start at minus the row's running
@@ -68,36 +69,33 @@ __device__ __forceinline__ uint32_t round2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
-template <int D, int WQ>
+template <int D>
 struct PrefixCfg {
-    static constexpr int WT = 4 / WQ;                 // waves along the tokens
-    static constexpr int SUB = WT == 1 ? 2 : 1;       // tiles of 32 tokens of a wave in a step
-    static constexpr int TOK = 32 * WT * SUB;         // tokens of a step
-    static constexpr int U = TOK / 64;                // of them copied by a lane
-    static constexpr int NC = D / 8, CH = (NC + 3) / 4;  // 16-byte chunks of a token, fours of them
-    static constexpr int KS = D / 16, DT = CH;
-    static constexpr int TILE = TOK * CH * 64;        // bytes of a step's keys (or values)
+    static constexpr int SUB = 2, TOK = 32 * SUB;         // tiles of 32 tokens of a step, its tokens
+    static constexpr int U = TOK / 64;                    // of them copied by a lane
+    static constexpr int NC = D / 8, CH = (NC + 3) / 4;   // 16-byte chunks of a token, fours of them
+    static constexpr int KS = D / 16, DT = CH;            // steps of the first product, tiles of the second
+    static constexpr int TILE = TOK * CH * 64;            // bytes of a step's keys (or values)
     static constexpr int UT = D / 16, UI = (UT + 3) / 4;  // 16-byte loads of a token in 8 bits, of a lane
     static_assert(4 * TILE <= 128 * 1024, "two steps in LDS");
 };
 
 }  // namespace
 
-template <int D, bool FP8, int WQ, int TERMS>
-__global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kernel(PrefixArgs p) {
-    using C = PrefixCfg<D, WQ>;
+template <int D, bool FP8, int TERMS>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArgs p) {
+    using C = PrefixCfg<D>;
     const AttendArgs &a = p.a;
     __shared__ __attribute__((aligned(16))) char lds[4 * C::TILE];
     __shared__ int bad[4];  // a page of the step is outside the cache; by step % 4
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wq = wave % WQ, wt = wave / WQ;
     // workgroup -> (head, part, group of rows): those of one head and part read
     // the same keys and values and go to one die, ids going round the eight dies
     const uint32_t chunks = static_cast<uint32_t>(p.chunks), die = blockIdx.x % 8, local = blockIdx.x / 8;
     const uint32_t pair = local / chunks * 8 + die, chunk = local % chunks;
-    const uint32_t parts = static_cast<uint32_t>(a.prefix_parts / C::WT);
+    const uint32_t parts = static_cast<uint32_t>(a.prefix_parts);
     if (pair >= static_cast<uint32_t>(a.c.heads) * parts) return;
     const int h = static_cast<int>(pair / parts), part = static_cast<int>(pair % parts);
     const int per = a.q_heads / a.c.heads;
@@ -105,7 +103,7 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
     const int tokens = static_cast<int>(last - first), steps = (tokens + C::TOK - 1) / C::TOK;
 
     // this lane's row, and the tokens that it sees, counted from the part's first
-    const int64_t rows = a.B * per, r = (static_cast<int64_t>(chunk) * WQ + wq) * 32 + c32;
+    const int64_t rows = a.B * per, r = (static_cast<int64_t>(chunk) * 4 + wave) * 32 + c32;
     const int64_t rr = r < rows ? r : rows - 1, b = rr / per, hq = rr % per;
     const int64_t n = a.lengths[b];
     int lo = 0, hi = 0;
@@ -205,8 +203,11 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
 
     // where this lane's pieces lie: chunk 2 i + half of token c32 (i even, i odd), and 4 elements of a V row for
     // each of two rows eight apart
-    const int row0 = wt * C::SUB * 32;
     int kat[2], vat[2];
+    // Zero, hidden from the compiler: where it knows the reads' places it keeps many of them in registers, 85 more
+    // than there are.
+    int row0 = 0;
+    asm volatile("" : "+s"(row0));
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         kat[x] = ((row0 + c32) / 16 * C::CH) * 1024 + c16 * 64 + (((2 * x + half) ^ (c16 / 4)) * 16);
@@ -377,7 +378,6 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
 #pragma unroll 1
         for (int64_t t = first; t < last; ++t) {
             const int at = static_cast<int>(t - first);
-            if (C::WT > 1 && at / 32 % C::WT != wt) continue;  // another wave's token
             const int32_t pg = p.pages[t >> a.c.page_shift];
             if (pg < 0 || pg >= a.c.pages) continue;  // those that see it are NaN already
             const int64_t ke = pg * a.c.kp + (t & place_mask) * a.c.kt, ve = pg * a.c.vp + (t & place_mask) * a.c.vt;
@@ -420,7 +420,7 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
     }
     if (r >= rows) return;
     const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + hq;
-    float *to = a.ws + (row * (a.parts + a.prefix_parts) + a.parts + part * C::WT + wt) * (D + 4);
+    float *to = a.ws + (row * (a.parts + a.prefix_parts) + a.parts + part) * (D + 4);
 #pragma unroll
     for (int i = 0; i < C::DT; ++i)
 #pragma unroll
@@ -431,14 +431,11 @@ __global__ __launch_bounds__(256, D <= 128 && WQ == 4 ? 2 : 1) void prefix_kerne
     if (half == 0) *reinterpret_cast<u32x2 *>(to + D) = u32x2{__float_as_uint(m), __float_as_uint(l)};
 }
 
-#define PROJ_PREFIX_WQ(D, WQ)                                              \
-    template __global__ void prefix_kernel<D, false, WQ, 2>(PrefixArgs); \
-    template __global__ void prefix_kernel<D, false, WQ, 3>(PrefixArgs); \
-    template __global__ void prefix_kernel<D, true, WQ, 2>(PrefixArgs);  \
-    template __global__ void prefix_kernel<D, true, WQ, 3>(PrefixArgs);
-#define PROJ_PREFIX_INST(D)               \
-    PROJ_PREFIX_WQ(D, (D <= 128 ? 1 : 2)) \
-    PROJ_PREFIX_WQ(D, 4)
+#define PROJ_PREFIX_INST(D)                                            \
+    template __global__ void prefix_kernel<D, false, 2>(PrefixArgs); \
+    template __global__ void prefix_kernel<D, false, 3>(PrefixArgs); \
+    template __global__ void prefix_kernel<D, true, 2>(PrefixArgs);  \
+    template __global__ void prefix_kernel<D, true, 3>(PrefixArgs);
 PROJ_PREFIX_INST(64)
 PROJ_PREFIX_INST(80)
 PROJ_PREFIX_INST(96)
@@ -447,10 +444,10 @@ PROJ_PREFIX_INST(192)
 PROJ_PREFIX_INST(256)
 
 #ifndef __HIP_DEVICE_COMPILE__
-template <int D, int WQ>
+template <int D>
 static hipError_t enqueue_prefix(const PrefixArgs &p, int64_t grid, hipStream_t st) {
-    auto kernel = p.a.c.fp8 ? (p.a.out_dtype == OUT_F32 ? prefix_kernel<D, true, WQ, 3> : prefix_kernel<D, true, WQ, 2>)
-                            : (p.a.out_dtype == OUT_F32 ? prefix_kernel<D, false, WQ, 3> : prefix_kernel<D, false, WQ, 2>);
+    auto kernel = p.a.c.fp8 ? (p.a.out_dtype == OUT_F32 ? prefix_kernel<D, true, 3> : prefix_kernel<D, true, 2>)
+                            : (p.a.out_dtype == OUT_F32 ? prefix_kernel<D, false, 3> : prefix_kernel<D, false, 2>);
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, p);
     return hipGetLastError();
 }
@@ -464,11 +461,7 @@ static hipError_t launch_shared_dim(PrefixArgs p, hipStream_t st) {
     const int64_t own_rows = a.B * a.c.heads * a.chunks, most = most_groups(256);
     // room for parts of a row: at least one of its own and one of the prefix
     const int64_t held = static_cast<int64_t>(a.ws_bytes / (sizeof(float) * (D + 4))) / (a.B * a.q_heads);
-    // waves along the tokens where one has all the rows (each then has a part of its own): four, two where a step
-    // of four would not fit LDS
-    constexpr int kFew = D <= 128 ? 1 : 2;
-    const int wq = rows <= 32 && held > 4 / kFew ? kFew : 4, wt = 4 / wq;
-    p.chunks = static_cast<int>((rows + 32 * wq - 1) / (32 * wq));
+    p.chunks = static_cast<int>((rows + 127) / 128);
     if (held < 2 || own_rows > most - 7 * a.c.heads * a.chunks || a.B * a.q_heads > most ||
         (static_cast<int64_t>(a.c.heads) + 7) * p.chunks > most) {
         if (a.B == 1) return hipErrorOutOfMemory;
@@ -483,17 +476,17 @@ static hipError_t launch_shared_dim(PrefixArgs p, hipStream_t st) {
     const int64_t pairs = static_cast<int64_t>(a.c.heads) * p.chunks;
     int64_t parts = (2 * static_cast<int64_t>(a.cus) + pairs - 1) / pairs;
     if (parts > (a.prefix + 127) / 128) parts = (a.prefix + 127) / 128;
-    if (parts > (held - 1) / wt) parts = (held - 1) / wt;
+    if (parts > held - 1) parts = held - 1;
     if (parts < 1) parts = 1;
     p.part = ((a.prefix + parts - 1) / parts + 127) / 128 * 128;
     parts = a.prefix > p.part ? (a.prefix + p.part - 1) / p.part : 1;
-    a.prefix_parts = static_cast<int>(parts * wt);
+    a.prefix_parts = static_cast<int>(parts);
     if (longest > 0) {
         const int64_t room = held - a.prefix_parts, most_parts = (most - 7 * a.c.heads * a.chunks) / own_rows;
         plan_attend(a, longest, room < most_parts ? room : most_parts);
     }
     const int64_t grid = (static_cast<int64_t>(a.c.heads) * parts + 7) / 8 * 8 * p.chunks;
-    hipError_t e = wq == kFew ? enqueue_prefix<D, kFew>(p, grid, st) : enqueue_prefix<D, 4>(p, grid, st);
+    hipError_t e = enqueue_prefix<D>(p, grid, st);
     if (e == hipSuccess && longest > 0) e = launch_attend_parts(a, st);
     return e != hipSuccess ? e : launch_attend_join(a, st);
 }

@@ -193,10 +193,8 @@ def test_attention_of_any_batch(host, B, q_heads, heads, dim, prefix, own, ws):
             assert f("lengths") == (3 << 40) + 4 * at and f("out") == (4 << 40) + 4 * at * q_heads * dim
             assert f("lse") == (5 << 40) + 4 * at * q_heads
             rows = f("B") * (q_heads // heads)
-            few = 4 if dim <= 128 else 2
-            wt = few if rows <= 32 and ws // row // f("B") > few else 1
-            assert f("chunks") * (128 // wt) >= rows and f("prefix_parts") % wt == 0
-            parts = f("prefix_parts") // wt
+            assert f("chunks") * 128 >= rows and f("block") == 256
+            parts = f("prefix_parts")
             assert parts * f("prefix_part") >= prefix and (parts - 1) * f("prefix_part") < prefix
             assert f("grid") >= heads * parts * f("chunks")
             assert f("parts") * f("part") >= own and (own == 0) == (f("parts") == 0)
