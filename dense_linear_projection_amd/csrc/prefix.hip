@@ -31,12 +31,12 @@
 //     once, and every read below has its place in its offset. Position
 //     (c % 4) ^ (token / 4 % 4) of a four holds chunk c: 16 tokens at one chunk, and
 //     four chunks of 4 tokens, fall on different banks.
-//   * a probability enters as bf16 terms, two for bf16 results (16 of its bits: errors
-//     against 64 bits as with all 24; with one term, 12% faster for 256 sequences, they
-//     are 1.4 times as large) and three for fp32 ones.
-// 256 sequences of 64 query heads behind 32768 tokens (8 heads of 128, bf16) 375 to 436 us
-// for the prefix, 0.63 to 0.73e15 operations a second of the formula's; the matrix cores
-// work in half of the cycles, vector instructions issue in the other half.
+//   * a probability enters as three bf16 terms, which together are its 24 bits, whatever
+//     the results' type, as in attend.hip. Two are faster (a call of 256 sequences behind
+//     32768 tokens 502 us instead of 586, of 64 behind 8192 80 instead of 84.5), but a few
+//     of a thousand bf16 results are then not the fp32 ones rounded.
+// 256 sequences of 64 query heads behind 32768 tokens (8 heads of 128, bf16) about 460 us
+// for the prefix, 0.6e15 operations a second of the formula's.
 #include <type_traits>
 
 #include "layer.hpp"
@@ -48,6 +48,7 @@ typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
 
 namespace {
 
+constexpr int kTerms = 3;  // bf16 terms of a probability
 constexpr float kLowest = -0x1.fffffep127f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -82,7 +83,7 @@ struct PrefixCfg {
 
 }  // namespace
 
-template <int D, bool FP8, int TERMS>
+template <int D, bool FP8>
 __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArgs p) {
     using C = PrefixCfg<D>;
     const AttendArgs &a = p.a;
@@ -291,20 +292,20 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
 #pragma unroll
                 for (int x = 0; x < C::SUB; ++x) s[x] -= by;
             }
-            bf16x8 prob[C::SUB][TERMS][2];
+            bf16x8 prob[C::SUB][kTerms][2];
 #pragma unroll
             for (int x = 0; x < C::SUB; ++x) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    uint32_t bits[TERMS][4];
+                    uint32_t bits[kTerms][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float p0 = __builtin_amdgcn_exp2f(s[x][8 * y + 2 * i] * c), p1 = __builtin_amdgcn_exp2f(s[x][8 * y + 2 * i + 1] * c);
                         l += p0;
                         l += p1;
 #pragma unroll
-                        for (int k = 0; k < TERMS; ++k) {
-                            if (k + 1 == TERMS) {
+                        for (int k = 0; k < kTerms; ++k) {
+                            if (k + 1 == kTerms) {
                                 bits[k][i] = round2(p0, p1);
                             } else {
                                 bits[k][i] = cut2(p0, p1);
@@ -314,7 +315,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < TERMS; ++k)
+                    for (int k = 0; k < kTerms; ++k)
                         prob[x][k][y] = __builtin_bit_cast(bf16x8, u32x4{bits[k][0], bits[k][1], bits[k][2], bits[k][3]});
                 }
             }
@@ -333,12 +334,12 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
                                 (__attribute__((address_space(3))) s16x4 *)(vt + vat[j] + (2 * x + y) * C::CH * 1024 + i * 1024));
                         const bf16x8 v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(z[0], z[1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-                        for (int k = 0; k < TERMS; ++k) o[i] = mfma32x32x16(v, prob[x][k][y], o[i]);
+                        for (int k = 0; k < kTerms; ++k) o[i] = mfma32x32x16(v, prob[x][k][y], o[i]);
                     }
             // the last step's are of no use, but a branch would part the matrix operations
             multiply(lds + ((step + 1) & 1) * 2 * C::TILE);
             // LDS reads eight ahead of the operations that need them
-            constexpr int READS = C::SUB * (4 * C::DT + C::KS), PRODUCTS = C::SUB * (2 * C::DT * TERMS + C::KS), AHEAD = 8;
+            constexpr int READS = C::SUB * (4 * C::DT + C::KS), PRODUCTS = C::SUB * (2 * C::DT * kTerms + C::KS), AHEAD = 8;
             __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
 #pragma unroll
             for (int i = 0; i < READS - AHEAD; ++i) {
@@ -431,11 +432,9 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
     if (half == 0) *reinterpret_cast<u32x2 *>(to + D) = u32x2{__float_as_uint(m), __float_as_uint(l)};
 }
 
-#define PROJ_PREFIX_INST(D)                                            \
-    template __global__ void prefix_kernel<D, false, 2>(PrefixArgs); \
-    template __global__ void prefix_kernel<D, false, 3>(PrefixArgs); \
-    template __global__ void prefix_kernel<D, true, 2>(PrefixArgs);  \
-    template __global__ void prefix_kernel<D, true, 3>(PrefixArgs);
+#define PROJ_PREFIX_INST(D)                                       \
+    template __global__ void prefix_kernel<D, false>(PrefixArgs); \
+    template __global__ void prefix_kernel<D, true>(PrefixArgs);
 PROJ_PREFIX_INST(64)
 PROJ_PREFIX_INST(80)
 PROJ_PREFIX_INST(96)
@@ -446,8 +445,7 @@ PROJ_PREFIX_INST(256)
 #ifndef __HIP_DEVICE_COMPILE__
 template <int D>
 static hipError_t enqueue_prefix(const PrefixArgs &p, int64_t grid, hipStream_t st) {
-    auto kernel = p.a.c.fp8 ? (p.a.out_dtype == OUT_F32 ? prefix_kernel<D, true, 3> : prefix_kernel<D, true, 2>)
-                            : (p.a.out_dtype == OUT_F32 ? prefix_kernel<D, false, 3> : prefix_kernel<D, false, 2>);
+    auto kernel = p.a.c.fp8 ? prefix_kernel<D, true> : prefix_kernel<D, false>;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, p);
     return hipGetLastError();
 }

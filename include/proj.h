@@ -439,9 +439,7 @@ proj_status proj_kv_attend(proj_ctx *ctx, const proj_kv_cache *cache, const void
  * and value of the prefix is read once for groups of 128 query rows of the
  * batch, not once for every sequence. Definition, types, alignment, padding
  * places and errors otherwise as proj_kv_attend; a page of the prefix outside
- * the cache makes those sequences NaN that see a token of it. Probabilities of
- * the prefix meet the values with 24 bits for fp32 results and with 16 for bf16
- * ones, which have 8. The workspace holds the fp32 results of the prefix's and
+ * the cache makes those sequences NaN that see a token of it. The workspace holds the fp32 results of the prefix's and
  * the sequences' parts: PROJ_ERR_NO_MEMORY (nothing enqueued) where it does not
  * hold two of (head_dim + 4) * 4 bytes for every query head of one sequence. */
 proj_status proj_kv_attend_shared(proj_ctx *ctx, const proj_kv_cache *cache, const void *q, int64_t q_stride, int64_t B,
