@@ -44,9 +44,11 @@
 // factor of 148): sums stay in range, and most tiles need no rescaling and no
 // exchange between lanes.  Logits are kept in natural units, and scaled to base
 // 2 once the maximum is taken off: scaled first, those past 2.36e38 overflowed.
+// Rows whose sums pass the largest float are worked out again (parts.hpp).
 #include <type_traits>
 
 #include "decode.hpp"
+#include "parts.hpp"
 
 namespace proj {
 
@@ -113,10 +115,10 @@ __device__ __forceinline__ int parts_of(const AttendArgs &a, int64_t n) {
     return static_cast<int>((n - a.prefix - first_seen(a, n) + a.part - 1) / a.part);
 }
 
-// Four elements of a finished head (and, with the first, its logarithm of the sum).
+// Four elements of a finished head (and, with the first, its logarithm of the sum); v are sums, or means already.
 __device__ __forceinline__ void finish_head(const AttendArgs &a, int64_t at, int64_t row, int d, f32x4 v, float most,
-                                            float total) {
-    const float f = total == 0.f ? 0.f : a.c.v_scale / total;
+                                            float total, bool mean = false) {
+    const float f = total == 0.f ? 0.f : mean ? a.c.v_scale : a.c.v_scale / total;
     v = total == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * f;
     if (a.out_dtype == OUT_F32) {
         *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = v;
@@ -143,14 +145,23 @@ __device__ __forceinline__ float2 get_part(const float *from) {
     return float2{__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32))};
 }
 
-// Two workgroups to a compute unit where their registers (and 160 KB of LDS) allow it.
+__device__ __forceinline__ void put_float(float *to, float x, int shared) {
+    if (shared)
+        __hip_atomic_store(to, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else
+        *to = x;
+}
+
+// Two workgroups to a compute unit, or three, where their registers (and 160 KB of LDS) allow it.
 template <int D, bool FP8, int QT, bool ONCE>
-__global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, D <= 64 ? 3 : D * QT <= 128 ? 2 : 1) void attend_kernel(AttendArgs a) {
     using C = AttendCfg<D, FP8, QT>;
     __shared__ __attribute__((aligned(16))) char lds[C::LDS];
     __shared__ uint32_t pages[kChunk + 2];
     __shared__ float top[4][16], sum[4][16];
     __shared__ int wrong, is_last;
+    __shared__ uint32_t again[QT];  // heads of a tile whose sums passed the largest float
+    static_assert(C::LDS >= kRowMeanLds, "room for row_mean");
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -176,6 +187,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
     const int64_t first = first_seen(a, n) + part * a.part;
     const int64_t last = parts == 0 ? first : n - a.prefix < first + a.part ? n - a.prefix : first + a.part;
     if (tid == 0) wrong = n < 0 || n > a.max_len;
+    if (tid < QT) again[tid] = 0;
 
     bf16x8 q[QT][C::KS];
 #pragma unroll
@@ -398,6 +410,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                 total = nan;
                 v = f32x4{nan, nan, nan, nan};
             }
+            if (past_largest(v, total)) atomicOr(&again[t], 1u << hq);
             const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + q0 + 16 * t + hq;
             if (parts > 1 || a.prefix_parts > 0) {
                 float *to = a.ws + (row * (a.parts + a.prefix_parts) + part) * (D + 4);
@@ -406,6 +419,27 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
                 if (d == 0) put_part(to + D, most, total, a.join);
             } else {
                 finish_head(a, row * D + d, row, d, v, most, total);
+            }
+        }
+    }
+    __syncthreads();
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) any |= again[t] != 0;
+    if (any) {
+        wait_vm<0>();  // what is stored again below has been stored
+        __syncthreads();
+        for (int x = 0; x < 16 * QT; ++x) {
+            if (!(again[x / 16] >> x % 16 & 1)) continue;
+            const int64_t hq = static_cast<int64_t>(h) * per + q0 + x, row = b * a.q_heads + hq;
+            const RowMean r = row_mean<D, FP8>(a.c, a.tables + b * a.table_stride, a.q + b * a.q_stride + hq * D, h, first, last,
+                                                  static_cast<double>(a.scale) * a.c.k_scale, lds);
+            if (parts > 1 || a.prefix_parts > 0) {
+                float *to = a.ws + (row * (a.parts + a.prefix_parts) + part) * (D + 4);
+                if (tid < D) put_float(to + tid, r.mean, a.join);
+                if (tid < 2) put_float(to + D + tid, tid == 0 ? r.most : -r.total, a.join);
+            } else if (tid < D) {
+                store_out(a.out, a.out_dtype, row * D + tid, r.mean * a.c.v_scale);
             }
         }
     }
@@ -432,7 +466,7 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
         const int d = e % (D / 4) * 4;
         const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + q0 + e / (D / 4);
         const float *from = a.ws + row * a.parts * (D + 4);
-        float most = kLowest, total = 0.f;
+        float most = kLowest, total = 0.f, least = 0.f;  // least: below zero where a part holds means
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (int p = 0; p < parts; ++p) most = fmaxf(most, get_part(from + p * (D + 4) + D).x);
@@ -441,10 +475,21 @@ __global__ __launch_bounds__(256, D * QT <= 128 ? 2 : 1) void attend_kernel(Atte
             const float *x = from + p * (D + 4);
             const float2 ml = get_part(x + D), lo = get_part(x + d), hi = get_part(x + d + 2);
             const float f = exp_above(ml.x, most);
-            total += ml.y * f;
+            total += fabsf(ml.y) * f;
+            least = fminf(least, ml.y);
             v += f32x4{lo.x, lo.y, hi.x, hi.y} * f;
         }
-        finish_head(a, row * D + d, row, d, v, most, total);
+        const bool mean = least < 0.f || past_largest(v, total);
+        if (mean) {
+            v = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int p = 0; p < parts; ++p) {
+                const float *x = from + p * (D + 4);
+                const float2 ml = get_part(x + D), lo = get_part(x + d), hi = get_part(x + d + 2);
+                const float f = exp_above(ml.x, most) / total;
+                v += f32x4{lo.x, lo.y, hi.x, hi.y} * (ml.y < 0.f ? f * -ml.y : f);
+            }
+        }
+        finish_head(a, row * D + d, row, d, v, most, total, mean);
     }
 }
 
@@ -474,30 +519,44 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a) {
     const int slice = tid / COLS, d = tid % COLS * 4;
     if (slice < SLICES) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        float total = 0.f;
+        float total = 0.f, least = 0.f;  // least: below zero where a part holds means
         for (int p = slice; p < parts; p += SLICES) {
             const float *x = from + place(p);
             const float f = exp_above(x[D], most);
             v += *reinterpret_cast<const f32x4 *>(x + d) * f;
-            total += x[D + 1] * f;
+            total += fabsf(x[D + 1]) * f;
+            least = fminf(least, x[D + 1]);
         }
         *reinterpret_cast<f32x4 *>(&red[slice][d]) = v;
-        if (d == 0) red[slice][D] = total;
+        if (d == 0) {
+            red[slice][D] = total;
+            red[slice][D + 1] = least;
+        }
     }
     __syncthreads();
     if (tid >= COLS) return;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    float total = 0.f;
+    float total = 0.f, least = 0.f;
 #pragma unroll
     for (int s = 0; s < SLICES; ++s) {
         v += *reinterpret_cast<const f32x4 *>(&red[s][d]);
         total += red[s][D];
+        least = fminf(least, red[s][D + 1]);
+    }
+    const bool mean = least < 0.f || past_largest(v, total);
+    if (mean) {
+        v = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < parts; ++p) {
+            const float *x = from + place(p);
+            const float l = x[D + 1], f = exp_above(x[D], most) / total;
+            v += *reinterpret_cast<const f32x4 *>(x + d) * (l < 0.f ? f * -l : f);
+        }
     }
     if (n < 0 || n > a.max_len) {
         total = __builtin_nanf("");
         v = f32x4{total, total, total, total};
     }
-    finish_head(a, row * D + d, row, d, v, most, total);
+    finish_head(a, row * D + d, row, d, v, most, total, mean);
 }
 
 // Instantiated here: the launchers below are compiled for the host only.

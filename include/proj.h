@@ -420,7 +420,8 @@ proj_status proj_kv_append_norm(proj_ctx *ctx, const proj_kv_cache *cache, const
  * contiguous, 16-byte aligned, q_stride a multiple of 8; out (16-byte aligned) fp32 or bf16 [B][q_heads][head_dim];
  * lse fp32 [B][q_heads] or NULL.  Sums and softmax are fp32,
  * and a probability meets the values with all of its 24 bits: bf16 results are
- * the fp32 ones, rounded.  The split over the length follows from B, heads, max_len, window and the context's workspace,
+ * the fp32 ones, rounded.  Where sums of large values pass the largest float, or
+ * values are not finite, the row is worked out again in 64 bits.  The split over the length follows from B, heads, max_len, window and the context's workspace,
  * which holds the parts' fp32 results (with none, nothing is split): the same
  * call gives the same bits every time.  Allocates nothing and never
  * synchronises. */
