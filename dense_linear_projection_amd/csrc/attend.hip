@@ -160,8 +160,8 @@ __global__ __launch_bounds__(256, D <= 64 ? 3 : D * QT <= 128 ? 2 : 1) void atte
     __shared__ uint32_t pages[kChunk + 2];
     __shared__ float top[4][16], sum[4][16];
     __shared__ int wrong, is_last;
-    __shared__ uint32_t again[QT];  // heads of a tile whose sums passed the largest float
-    static_assert(C::LDS >= kRowMeanLds, "room for row_mean");
+    __shared__ uint32_t again;  // heads (bits, of 16 QT) whose sums are not finite
+    static_assert(C::LDS >= rows_again_lds(D) && QT <= 2, "room for rows_again, and for the bits");
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256, D <= 64 ? 3 : D * QT <= 128 ? 2 : 1) void atte
     const int64_t first = first_seen(a, n) + part * a.part;
     const int64_t last = parts == 0 ? first : n - a.prefix < first + a.part ? n - a.prefix : first + a.part;
     if (tid == 0) wrong = n < 0 || n > a.max_len;
-    if (tid < QT) again[tid] = 0;
+    if (tid == 0) again = 0;
 
     bf16x8 q[QT][C::KS];
 #pragma unroll
@@ -410,7 +410,7 @@ __global__ __launch_bounds__(256, D <= 64 ? 3 : D * QT <= 128 ? 2 : 1) void atte
                 total = nan;
                 v = f32x4{nan, nan, nan, nan};
             }
-            if (past_largest(v, total)) atomicOr(&again[t], 1u << hq);
+            if (__builtin_expect(past_largest(v, total), 0)) atomicOr(&again, 1u << (16 * t + hq));
             const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + q0 + 16 * t + hq;
             if (parts > 1 || a.prefix_parts > 0) {
                 float *to = a.ws + (row * (a.parts + a.prefix_parts) + part) * (D + 4);
@@ -423,25 +423,22 @@ __global__ __launch_bounds__(256, D <= 64 ? 3 : D * QT <= 128 ? 2 : 1) void atte
         }
     }
     __syncthreads();
-    bool any = false;
-#pragma unroll
-    for (int t = 0; t < QT; ++t) any |= again[t] != 0;
-    if (any) {
-        wait_vm<0>();  // what is stored again below has been stored
-        __syncthreads();
-        for (int x = 0; x < 16 * QT; ++x) {
-            if (!(again[x / 16] >> x % 16 & 1)) continue;
-            const int64_t hq = static_cast<int64_t>(h) * per + q0 + x, row = b * a.q_heads + hq;
-            const RowMean r = row_mean<D, FP8>(a.c, a.tables + b * a.table_stride, a.q + b * a.q_stride + hq * D, h, first, last,
-                                                  static_cast<double>(a.scale) * a.c.k_scale, lds);
-            if (parts > 1 || a.prefix_parts > 0) {
-                float *to = a.ws + (row * (a.parts + a.prefix_parts) + part) * (D + 4);
-                if (tid < D) put_float(to + tid, r.mean, a.join);
-                if (tid < 2) put_float(to + D + tid, tid == 0 ? r.most : -r.total, a.join);
-            } else if (tid < D) {
-                store_out(a.out, a.out_dtype, row * D + tid, r.mean * a.c.v_scale);
-            }
-        }
+    if (__builtin_expect(again != 0, 0)) {
+        wait_vm<0>();  // what is stored again has been stored
+        const int64_t head0 = static_cast<int64_t>(h) * per + q0;
+        rows_again<D, FP8>(
+            a.c, a.tables + b * a.table_stride, h, static_cast<double>(a.scale) * a.c.k_scale, &again, 1, lds,
+            [&](int x) { return RowAgain{a.q + b * a.q_stride + (head0 + x) * D, first, last}; },
+            [&](int x, int d, const RowMean &y) {
+                const int64_t row = b * a.q_heads + head0 + x;
+                if (parts > 1 || a.prefix_parts > 0) {
+                    float *to = a.ws + (row * (a.parts + a.prefix_parts) + part) * (D + 4);
+                    put_float(to + d, y.mean, a.join);
+                    if (d < 2) put_float(to + D + d, d == 0 ? y.most : -y.total, a.join);
+                } else {
+                    store_out(a.out, a.out_dtype, row * D + d, y.mean * a.c.v_scale);
+                }
+            });
     }
     if (!a.join || parts <= 1) return;
 
@@ -480,7 +477,7 @@ __global__ __launch_bounds__(256, D <= 64 ? 3 : D * QT <= 128 ? 2 : 1) void atte
             v += f32x4{lo.x, lo.y, hi.x, hi.y} * f;
         }
         const bool mean = least < 0.f || past_largest(v, total);
-        if (mean) {
+        if (__builtin_expect(mean, 0)) {
             v = f32x4{0.f, 0.f, 0.f, 0.f};
             for (int p = 0; p < parts; ++p) {
                 const float *x = from + p * (D + 4);

@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "layer.hpp"
+#include "parts.hpp"
 
 namespace proj {
 
@@ -89,6 +90,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
     const AttendArgs &a = p.a;
     __shared__ __attribute__((aligned(16))) char lds[4 * C::TILE];
     __shared__ int bad[4];  // a page of the step is outside the cache; by step % 4
+    __shared__ uint32_t again[4];  // rows of each wave whose sums are not finite
+    static_assert(4 * C::TILE >= rows_again_lds(D), "room for rows_again");
 
     const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, c32 = lane & 31, c16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -359,56 +362,17 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
     const float top = -negm[0];
 
     // A sum that is not finite though its probabilities are: a value met a
-    // probability of zero (a token that another row sees) or a vanished term.
-    // Such rows are worked out again from the definition, a token at a time,
-    // taking nothing from where the probability is zero.
+    // probability of zero (a token that another row sees) or a vanished term, or
+    // sums passed the largest float. Such rows are worked out again, below.
     float check = 0.f;
 #pragma unroll
     for (int i = 0; i < C::DT; ++i)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
             if (32 * i + 8 * (v / 4) + 4 * half < D) check += o[i][v] * 0.f;
-    check += __shfl_xor(check, 32, 64);  // a row's two lanes go together: they exchange halves of its logits
-    const bool again = !(check == 0.f) && l == l && !none;  // infinity times 0 is NaN
-    if (__any(again)) {
-        if (again)
-#pragma unroll
-            for (int i = 0; i < C::DT; ++i)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) o[i][v] = 0.f;
-#pragma unroll 1
-        for (int64_t t = first; t < last; ++t) {
-            const int at = static_cast<int>(t - first);
-            const int32_t pg = p.pages[t >> a.c.page_shift];
-            if (pg < 0 || pg >= a.c.pages) continue;  // those that see it are NaN already
-            const int64_t ke = pg * a.c.kp + (t & place_mask) * a.c.kt, ve = pg * a.c.vp + (t & place_mask) * a.c.vt;
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < C::KS; ++i) {
-                const u32x4 qb = __builtin_bit_cast(u32x4, q[i]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t x = ke + 16 * i + 8 * half + e;
-                    const float k = FP8 ? __builtin_amdgcn_cvt_f32_fp8(reinterpret_cast<const uint8_t *>(kb)[x], 0)
-                                        : bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(kb)[x]);
-                    dot = __builtin_fmaf(k, __uint_as_float(e % 2 ? qb[e / 2] & 0xffff0000u : qb[e / 2] << 16), dot);
-                }
-            }
-            dot += __shfl_xor(dot, 32, 64);
-            const float prob = at >= lo && at < hi ? __builtin_amdgcn_exp2f((dot - top) * c) : 0.f;
-            if (!again || prob == 0.f) continue;
-#pragma unroll
-            for (int i = 0; i < C::DT; ++i)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int d = 32 * i + 8 * (v / 4) + 4 * half + v % 4;
-                    if (d >= D) continue;
-                    const float x = FP8 ? __builtin_amdgcn_cvt_f32_fp8(reinterpret_cast<const uint8_t *>(vb)[ve + d], 0)
-                                        : bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(vb)[ve + d]);
-                    o[i][v] = __builtin_fmaf(prob, x, o[i][v]);
-                }
-        }
-    }
+    check += __shfl_xor(check, 32, 64);
+    const uint64_t marks = __ballot(!(check == 0.f) && l == l && !none);  // infinity times 0 is NaN
+    if (lane == 0) again[wave] = static_cast<uint32_t>(marks);
 
     float m = above < 0.f ? kLowest : top * to_logit;
     if (none) {
@@ -419,17 +383,37 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
 #pragma unroll
             for (int v = 0; v < 16; ++v) o[i][v] = 0.f;
     }
-    if (r >= rows) return;
-    const int64_t row = b * a.q_heads + static_cast<int64_t>(h) * per + hq;
-    float *to = a.ws + (row * (a.parts + a.prefix_parts) + a.parts + part) * (D + 4);
+    auto part_of = [&](int64_t b, int64_t hq) {
+        return a.ws + ((b * a.q_heads + static_cast<int64_t>(h) * per + hq) * (a.parts + a.prefix_parts) + a.parts + part) * (D + 4);
+    };
+    if (r < rows) {
+        float *to = part_of(b, hq);
 #pragma unroll
-    for (int i = 0; i < C::DT; ++i)
+        for (int i = 0; i < C::DT; ++i)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const int d = 32 * i + 8 * y + 4 * half;
-            if (d < D) *reinterpret_cast<f32x4 *>(to + d) = f32x4{o[i][4 * y], o[i][4 * y + 1], o[i][4 * y + 2], o[i][4 * y + 3]};
-        }
-    if (half == 0) *reinterpret_cast<u32x2 *>(to + D) = u32x2{__float_as_uint(m), __float_as_uint(l)};
+            for (int y = 0; y < 4; ++y) {
+                const int d = 32 * i + 8 * y + 4 * half;
+                if (d < D) *reinterpret_cast<f32x4 *>(to + d) = f32x4{o[i][4 * y], o[i][4 * y + 1], o[i][4 * y + 2], o[i][4 * y + 3]};
+            }
+        if (half == 0) *reinterpret_cast<u32x2 *>(to + D) = u32x2{__float_as_uint(m), __float_as_uint(l)};
+    }
+    __syncthreads();
+    if ((again[0] | again[1] | again[2] | again[3]) == 0) return;
+    wait_vm<0>();  // what is stored again has been stored
+    rows_again<D, FP8>(
+        a.c, p.pages, h, static_cast<double>(a.scale) * a.c.k_scale, again, 4, lds,
+        [&](int x) {
+            const int64_t at = static_cast<int64_t>(chunk) * 128 + x, bx = at / per, nx = a.lengths[bx];
+            const int64_t low = a.window > 0 && nx > a.window ? nx - a.window : 0;
+            return RowAgain{a.q + bx * a.q_stride + (static_cast<int64_t>(h) * per + at % per) * D, low > first ? low : first,
+                            nx < last ? nx : last};
+        },
+        [&](int x, int d, const RowMean &y) {
+            const int64_t at = static_cast<int64_t>(chunk) * 128 + x;
+            float *to = part_of(at / per, at % per);
+            to[d] = y.mean;
+            if (d < 2) to[D + d] = d == 0 ? y.most : -y.total;
+        });
 }
 
 #define PROJ_PREFIX_INST(D)                                       \
