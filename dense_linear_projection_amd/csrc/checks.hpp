@@ -2,6 +2,7 @@
 // share (decode.cpp, layer.cpp).
 #pragma once
 
+#include <cfloat>
 #include <climits>
 #include <utility>
 
@@ -150,6 +151,9 @@ inline proj_status check_attend(proj_ctx *ctx, const proj_kv_cache *cache, const
                              (long long)q_stride, (long long)width);
     if (!(scale == scale) || scale > 3e38f || scale < -3e38f)
         return context_error(ctx, PROJ_ERR_INVALID_ARG, "scale is not finite");
+    if (!(static_cast<double>(scale < 0.f ? -scale : scale) * cache->k_scale <= static_cast<double>(FLT_MAX)))
+        return context_error(ctx, PROJ_ERR_INVALID_ARG, "scale %g times the cache's k_scale %g is past the largest float",
+                             (double)scale, (double)cache->k_scale);
     if (B == 0) return PROJ_OK;
     if (q_stride > kMost / B || table_stride > kMost / B)
         return context_error(ctx, PROJ_ERR_UNSUPPORTED, "q or tables too large");

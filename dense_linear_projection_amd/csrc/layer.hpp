@@ -48,6 +48,8 @@ struct PrefixArgs {
     // set by the launcher: tokens of a part, groups of rows that one workgroup takes
     int64_t part = 0;
     int chunks = 0;
+    // and what makes a logit of <q, k>: to_logit up, down one over up
+    float to_logit = 1.f, up = 1.f, down = 1.f;
 };
 hipError_t launch_attend_shared(const PrefixArgs &p, hipStream_t st);
 

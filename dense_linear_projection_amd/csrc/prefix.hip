@@ -25,7 +25,9 @@
 //   * vector instructions and matrix ones take about the same time here, so the
 //     former are what counts. Logits stay in units of <q, k>, and the scale comes in
 //     the exponent; the maximum moves only when a logit passes it by more than 5
-//     (a factor of 148); the sign of the scale is put into q.
+//     (a factor of 148); the sign of the scale is put into q. Where the scale in base 2
+//     passes the range of a float, differences from the maximum are first multiplied by
+//     a power of two.
 //   * in LDS, tokens lie in sixteens, within those the 16-byte chunks of a token in
 //     fours: a lane copies chunks of one token only, whose address it works out
 //     once, and every read below has its place in its offset. Position
@@ -37,6 +39,7 @@
 //     of a thousand bf16 results are then not the fp32 ones rounded.
 // 256 sequences of 64 query heads behind 32768 tokens (8 heads of 128, bf16) about 460 us
 // for the prefix, 0.6e15 operations a second of the formula's.
+#include <cmath>
 #include <type_traits>
 
 #include "layer.hpp"
@@ -117,16 +120,26 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
         hi = static_cast<int>((n < first ? first : n < last ? n : last) - first);
     }
     const bool none = hi <= lo;  // a row that sees nothing here: computed with the others, and dropped
-    // logits are to_logit <q, k>, q with the scale's sign (and zero, with the scale 1, for a scale of zero)
-    const float to_logit = a.scale == 0.f ? 1.f : fabsf(a.scale) * a.c.k_scale, c = to_logit * kLog2e, enough = 5.f / to_logit;
-    const uint32_t keep = a.scale == 0.f ? 0u : ~0u, flip = a.scale < 0.f ? 0x80008000u : 0u;
+    // logits are to_logit up <q, k>, q with the scale's sign (and 0 times it, with the scale 1, for a scale of zero)
+    const float to_logit = p.to_logit, c = to_logit * kLog2e, enough = 5.f / to_logit;
+    const bool far = p.up != 1.f;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     bf16x8 q[C::KS];
 #pragma unroll
     for (int i = 0; i < C::KS; ++i) {
         u32x4 w = __builtin_bit_cast(u32x4, load16(a.q + b * a.q_stride + (static_cast<int64_t>(h) * per + hq) * D + 16 * i + 8 * half));
-        w = (w & keep) ^ flip;
+        w ^= flip;
         q[i] = __builtin_bit_cast(bf16x8, w);
     }
+    if (__builtin_expect(a.scale == 0.f, 0))
+#pragma unroll
+        for (int i = 0; i < C::KS; ++i) {
+            u32x4 w = __builtin_bit_cast(u32x4, q[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // NaN where infinite or no number
+                w[e] = ((w[e] & 0x7f80u) == 0x7f80u ? 0x7fc0u : 0u) | ((w[e] & 0x7f800000u) == 0x7f800000u ? 0x7fc00000u : 0u);
+            q[i] = __builtin_bit_cast(bf16x8, w);
+        }
     f32x16 o[C::DT], negm;  // negm: minus the running maximum, from which a sum starts
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
@@ -263,8 +276,11 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
         next_pages(step + 3);
         const int t0 = step * C::TOK + row0;
         if (!idle) {
-            const bool whole = __all((lo <= t0 && hi >= t0 + 32 * C::SUB) || none) && t0 + 32 * C::SUB <= tokens && !any_bad;
+            const bool whole = __all((lo <= t0 && hi >= t0 + 32 * C::SUB) || none) && t0 + 32 * C::SUB <= tokens && !any_bad && !far;
             if (!whole) {
+                if (far)
+#pragma unroll
+                    for (int x = 0; x < C::SUB; ++x) s[x] *= p.up;
 #pragma unroll
                 for (int x = 0; x < C::SUB; ++x)
 #pragma unroll
@@ -291,7 +307,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < C::DT; ++i) o[i] *= f;
-                negm -= by;
+                negm -= by * p.down;
 #pragma unroll
                 for (int x = 0; x < C::SUB; ++x) s[x] -= by;
             }
@@ -374,7 +390,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void prefix_kernel(PrefixArg
     const uint64_t marks = __ballot(!(check == 0.f) && l == l && !none);  // infinity times 0 is NaN
     if (lane == 0) again[wave] = static_cast<uint32_t>(marks);
 
-    float m = above < 0.f ? kLowest : top * to_logit;
+    float m = above < 0.f ? kLowest : top * p.up * to_logit;
     if (none) {
         m = kLowest;
         l = 0.f;
@@ -473,7 +489,21 @@ static hipError_t launch_shared_dim(PrefixArgs p, hipStream_t st) {
     return e != hipSuccess ? e : launch_attend_join(a, st);
 }
 
-hipError_t launch_attend_shared(const PrefixArgs &p, hipStream_t st) {
+hipError_t launch_attend_shared(const PrefixArgs &args, hipStream_t st) {
+    PrefixArgs p = args;
+    // The scales' product, exact in 64 bits, as a float and (where that or its base-2 form may pass the ends of the
+    // range) a power of two. Below 2^-240 every finite logit is 0 beside the others, and so it is with that.
+    const double f = std::fabs(static_cast<double>(p.a.scale)) * p.a.c.k_scale;
+    if (p.a.scale == 0.f) {
+        p.to_logit = 1.f;
+    } else if (f > 0x1p-100 && f < 0x1p100) {
+        p.to_logit = static_cast<float>(f);
+    } else {
+        const int e = std::ilogb(f) > 120 ? 120 : std::ilogb(f) < -120 ? -120 : std::ilogb(f);
+        p.up = std::ldexp(1.f, e);
+        p.down = std::ldexp(1.f, -e);
+        p.to_logit = static_cast<float>((f < 0x1p-240 ? 0x1p-240 : f) * p.down);
+    }
     switch (p.a.c.dim) {
         case 64: return launch_shared_dim<64>(p, st);
         case 80: return launch_shared_dim<80>(p, st);
