@@ -134,14 +134,27 @@ __device__ __forceinline__ float scaled(int32_t sum, float xs, float ws) {
     return static_cast<float>(static_cast<double>(sum) * (static_cast<double>(xs) * ws));
 }
 
+// Bias and GELU of scaled sums. One GELU for every kernel, so that which of them runs does not show in the result.
+template <int N>
+__device__ __forceinline__ void finish(float (&v)[N], int epi, const float (&bias)[N]) {
+    if (epi & 1)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] += bias[e];
+    if (epi & 2)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = gelu_tanh_fast(v[e]);
+}
+
 // Four outputs of one token, before bias and GELU scaled already, written where they are there.
 __device__ __forceinline__ void write4(const IntArgs &a, int64_t m, int64_t n, const int32_t (&sum)[4], float xs) {
-    float v[4];
+    float v[4], bias[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int64_t col = n + r < a.N ? n + r : a.N - 1;
-        v[r] = apply_epilogue(scaled(sum[r], xs, a.w_scales[col]), a.epi, (a.epi & 1) ? bf16_bits_to_f32(a.bias[col]) : 0.f);
+        v[r] = scaled(sum[r], xs, a.w_scales[col]);
+        bias[r] = (a.epi & 1) ? bf16_bits_to_f32(a.bias[col]) : 0.f;
     }
+    finish(v, a.epi, bias);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (n + r < a.N) store_out(a.Y, a.out, m * a.row + n + r, v[r]);
@@ -577,11 +590,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2 * OCC, 2 
                 if (m >= a.M || n >= a.N) continue;
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[e] = scaled(acc[i][2 * j + e / 4][e % 4], xs[i], ws[e]);
-                    if (a.epi & 1) v[e] += bias[e];
-                    if (a.epi & 2) v[e] = gelu_tanh_fast(v[e]);
-                }
+                for (int e = 0; e < 8; ++e) v[e] = scaled(acc[i][2 * j + e / 4][e % 4], xs[i], ws[e]);
+                finish(v, a.epi, bias);
                 if (whole && n + 8 <= a.N && a.out == OUT_BF16) {
                     u32x4 y;
 #pragma unroll
@@ -612,8 +622,12 @@ PROJ_INT_TILE_VARIANTS(PROJ_INT_TILE_INST)
 
 // K = 0: the sum is empty.
 __global__ __launch_bounds__(256) void int_empty_kernel(IntArgs a) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < a.M * a.N; i += static_cast<int64_t>(gridDim.x) * 256)
-        store_out(a.Y, a.out, i, apply_epilogue(0.f, a.epi, (a.epi & 1) ? bf16_bits_to_f32(a.bias[i % a.N]) : 0.f));
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < a.M * a.N; i += static_cast<int64_t>(gridDim.x) * 256) {
+        float v[1] = {0.f};
+        const float bias[1] = {(a.epi & 1) ? bf16_bits_to_f32(a.bias[i % a.N]) : 0.f};
+        finish(v, a.epi, bias);
+        store_out(a.Y, a.out, i, v[0]);
+    }
 }
 
 #define PROJ_INT_STREAM_VARIANTS(X)                                                                       \
