@@ -192,7 +192,8 @@ proj_status proj_kv_attend_shared(proj_ctx *ctx, const proj_kv_cache *cache, con
     proj_status s = context_view(ctx, &v);
     if (s != PROJ_OK) return s;
     PrefixArgs p;
-    if (prefix_len < 0 || prefix_len > INT32_MAX || (prefix_len > 0 && B > 0 && !prefix) || !aligned(prefix, 4))
+    // the kernel counts the tokens of a part, which may be all of them, in 32 bits, up to a whole step
+    if (prefix_len < 0 || prefix_len > INT32_MAX - 127 || (prefix_len > 0 && B > 0 && !prefix) || !aligned(prefix, 4))
         return context_error(ctx, PROJ_ERR_INVALID_ARG, "prefix of %lld tokens, or its pages NULL or not aligned",
                              (long long)prefix_len);
     s = check_attend(ctx, cache, q, q_stride, B, q_heads, tables, table_stride, table_width, lengths, max_len, prefix_len,

@@ -435,7 +435,7 @@ proj_status proj_kv_attend(proj_ctx *ctx, const proj_kv_cache *cache, const void
  * token t < prefix_len of every sequence is in page prefix[t / page_size], place
  * t % page_size; token t >= prefix_len of sequence b is token t - prefix_len of
  * its own, in page tables[b * table_stride + (t - prefix_len) / page_size].
- * prefix_len need not be a multiple of page_size. lengths, max_len and window
+ * prefix_len, at most 2^31 - 128, need not be a multiple of page_size. lengths, max_len and window
  * count all of a sequence's tokens, so a length below prefix_len sees that much
  * of the prefix; the tables hold max_len - prefix_len tokens at least. Each key
  * and value of the prefix is read once for groups of 128 query rows of the
