@@ -176,8 +176,8 @@ constexpr uint32_t kOutside = 0x80000000u;
 //
 // FUSED: very few tokens come as bf16 rows, and every workgroup makes them integers
 // itself, in LDS, while its first stages of W are on their way: their bytes are few
-// beside W's, and a launch less counts more (one token, K8192 N1024: 9.5 us a call
-// against 11.8).
+// beside W's, and a launch less counts more (one token, K8192 N1024: 8.6 us a call
+// against 10.5).
 constexpr int kFusedRows = 4, kFusedK = 8192;  // rows whose chunks a workgroup's registers hold
 
 template <int MT, int NT, int WAVES, int KC, int D, bool FUSED = false>

@@ -73,7 +73,8 @@ __device__ __forceinline__ void load8_weights(const AppendArgs &a, const void *n
 // lanes of one wave, 4, 8 or 16 of them (those past D / 16 have no elements), and
 // exchange their sums of squares, which are fp32 unless they near its ends: then
 // 64 bits, so that no bf16 input overflows or vanishes (64 bits for all heads took
-// 78 us where the plain append takes 62, their conversions at a quarter of the rate).
+// 81 us where this takes 73, 8192 tokens back to back, their conversions at a quarter of
+// the rate).
 template <int PAIRING, int TOK, bool NORM>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a, uint32_t blocks) {
     const int D = a.c.dim, per = NORM ? a.norm_lanes : D / 16;
@@ -243,8 +244,8 @@ static hipError_t launch_append_as(AppendArgs a, hipStream_t st) {
     a.norm_share = 1.f / a.c.dim;
     const int64_t items = (static_cast<int64_t>(a.q_heads) + 2 * a.c.heads) * (NORM ? a.norm_lanes : a.c.dim / 16);
     const int64_t blocks = (items + 255) / 256;
-    // four tokens to a thread once that leaves enough threads for the chip; normed, one: the registers of four
-    // leave half as many waves (8192 tokens of 80 heads 74.5 us, with one 73.3)
+    // four tokens to a thread once that leaves enough threads for the chip; normed, one: four are no faster (8192
+    // tokens of 80 heads 73 us back to back with either, 65 alone)
     const int tok = !NORM && a.T * items >= (int64_t{1} << 20) ? 4 : 1;
     auto kernel = append_kernel<PAIRING, 1, NORM>;
     if constexpr (!NORM)

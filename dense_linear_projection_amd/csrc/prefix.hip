@@ -12,8 +12,8 @@
 // A workgroup is four waves on (key-value head, part, group of 128 rows), 32 rows to
 // a wave. Keys and values go into LDS in bf16 whatever the cache's type, 64 tokens
 // to a step, those of the next steps on their way while this one is computed. Waves
-// without rows only copy: with 32 rows in all, four waves on different tokens, each
-// with a part of its own, took 78 us for 65536 tokens where these take 58.
+// without rows only copy: with 8 rows in all, four waves on different tokens, each with
+// a part of its own, took 87 us a call for 65536 tokens where these took 68.
 //   * w: v_mfma_f32_32x32x16_bf16 with A = 32 tokens of K and B = 32 rows of q,
 //     held for the whole call. A lane of the result has row l % 32 and tokens
 //     8 (v / 4) + 4 (l / 32) + v % 4. The sums start at minus the row's running
@@ -37,8 +37,10 @@
 //     the results' type, as in attend.hip. Two are faster (a call of 256 sequences behind
 //     32768 tokens 502 us instead of 586, of 64 behind 8192 80 instead of 84.5), but a few
 //     of a thousand bf16 results are then not the fp32 ones rounded.
-// 256 sequences of 64 query heads behind 32768 tokens (8 heads of 128, bf16) about 460 us
-// for the prefix, 0.6e15 operations a second of the formula's.
+// 256 sequences of 64 query heads behind 32768 tokens (8 heads of 128, bf16) 480 to 524 us
+// for the prefix, 0.52 to 0.57e15 operations a second of the formula's; the matrix cores
+// work in 58% of the cycles, vector instructions issue in 52%. Every token of the prefix is
+// read, whatever lengths and a window leave of it.
 #include <cmath>
 #include <type_traits>
 

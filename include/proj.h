@@ -422,7 +422,8 @@ proj_status proj_kv_append_norm(proj_ctx *ctx, const proj_kv_cache *cache, const
  * lse fp32 [B][q_heads] or NULL.  Sums and softmax are fp32,
  * and a probability meets the values with all of its 24 bits: bf16 results are
  * the fp32 ones, rounded.  Where sums of large values pass the largest float, or
- * values are not finite, the row is worked out again in 64 bits.  The split over the length follows from B, heads, max_len, window and the context's workspace,
+ * values are not finite, the row is worked out again in 64 bits (0.66 ms instead of
+ * 0.07 where every row of 64 sequences of 2000 tokens is).  The split over the length follows from B, heads, max_len, window and the context's workspace,
  * which holds the parts' fp32 results (with none, nothing is split): the same
  * call gives the same bits every time.  Allocates nothing and never
  * synchronises. */
@@ -439,7 +440,10 @@ proj_status proj_kv_attend(proj_ctx *ctx, const proj_kv_cache *cache, const void
  * count all of a sequence's tokens, so a length below prefix_len sees that much
  * of the prefix; the tables hold max_len - prefix_len tokens at least. Each key
  * and value of the prefix is read once for groups of 128 query rows of the
- * batch, not once for every sequence. Definition, types, alignment, padding
+ * batch, not once for every sequence - all of them, whatever lengths and a window
+ * leave to be seen, and in three launches: proj_kv_attend on whole tables is the
+ * faster one for a single sequence, for up to 4 behind 2000 tokens or 64 behind
+ * 500, and for windows much shorter than the prefix. Definition, types, alignment, padding
  * places and errors otherwise as proj_kv_attend; a page of the prefix outside
  * the cache makes those sequences NaN that see a token of it. The workspace holds the fp32 results of the prefix's and
  * the sequences' parts: PROJ_ERR_NO_MEMORY (nothing enqueued) where it does not
