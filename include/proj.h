@@ -414,7 +414,8 @@ proj_status proj_kv_append_norm(proj_ctx *ctx, const proj_kv_cache *cache, const
  * the table or the cache, is not used, NaN included.  n above max_len, n < 0,
  * or a page of the range outside the cache: that sequence's out and lse are
  * NaN and nothing outside the cache is read.  scale times the cache's k_scale has
- * to be a finite float.  max_len (at most table_width *
+ * to be a finite float; a <q, k[t]> of the stored values past the largest float is
+ * infinite.  max_len (at most table_width *
  * page_size) bounds the lengths and shapes the launch: the parts of the length
  * are cut for sequences that long, so one far above the lengths leaves short
  * sequences few and long parts.  q bf16: row b at q + b * q_stride, heads

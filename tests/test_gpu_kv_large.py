@@ -4,6 +4,7 @@ result, their mean, does not."""
 import pytest
 import torch
 
+import dense_linear_projection_amd as dlp
 from tests import decode_reference as ref
 from tests.test_gpu_kv import BF16, F32, make_attend, run_attend
 
@@ -83,3 +84,29 @@ def test_infinite_and_large_values_together(ctx, out):
     keep[0, 2:, 7:9] = False
     ref.close(o.cpu()[keep], clean[0][keep], tol[0][keep])
     ref.close(lse, clean[1], tol[1])
+
+
+def test_replays_follow_their_inputs(ctx):
+    """Rows are worked out again, or not, as the values of the replay say; the counters of the joining are left at zero."""
+    lengths = [700, 3, 260, 0]
+    k, v, cache, q, tables, n, _ = make_attend(4, 8, 2, 128, 16, BF16, "hnd", lengths, 6, poison=False)
+    cache.k.copy_(k / 8)
+    dev = [t.cuda() for t in (q, tables, n)]
+    o, lse = torch.empty(4, 8, 128, device="cuda"), torch.empty(4, 8, device="cuda")
+
+    def call(o, lse):
+        dlp.proj_kv_attend(ctx, cache, *dev, 1.0, o, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(o, lse)
+    for size in (1.0, 1e38, 1.0, 1e37, 1.0):
+        cache.v.copy_((torch.rand(v.shape) + 1) * size)
+        o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = torch.empty_like(o), torch.empty_like(lse)
+        call(a, b)
+        torch.cuda.synchronize()
+        assert torch.equal(o, a) and torch.equal(lse, b)
+        want, tol = ref.attend(cache.k.cpu(), cache.v.cpu(), q, tables, n, 1.0, 0, (1, 1), F32)
+        ref.close(o, want[0], tol[0])
